@@ -20,6 +20,9 @@
 #include "decode.cuh"
 #include "fwd256.cuh"
 #include "bwd256.cuh"
+#include "kv4.cuh"
+#include "evict.cuh"
+#include "key_weights.cuh"
 
 namespace fa {
 // Self-test of the failure path: waits on an mbarrier that nothing will ever
@@ -725,3 +728,5 @@ int fa_check_status(void* stream) {
 }
 
 }  // extern "C"
+
+#include "api_cache.cuh"

@@ -281,3 +281,159 @@ def fa_decode(q, k, v, o, lse, scale: float, workspace, stream=None) -> None:
           o=(o, _bf, (B, H, d)), lse=(lse, _f32, (B, H)), workspace=(workspace, _u8, (int(workspace.numel()),)))
     _check(lib.fa_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, N, d, float(scale),
                          _ptr(workspace), int(workspace.numel()), _stream(stream)), "fa_decode")
+
+
+# ---- the 4-bit key/value cache ---------------------------------------------------------------------------------
+lib.fa_key_weights_workspace_bytes.restype = _sz
+lib.fa_key_weights_workspace_bytes.argtypes = [_ci] * 6
+lib.fa_key_weights.argtypes = [_vp] * 5 + [_ci] * 8 + [_cf, _vp, _sz, _vp]
+lib.fa_evict_keep.argtypes = [_vp] * 4 + [_ci] * 6 + [_vp]
+lib.fa_evict_slots.argtypes = [_vp] * 5 + [_ci] * 7 + [_vp]
+lib.fa_kv4_append.argtypes = [_vp] * 15 + [_ci] * 7 + [_vp]
+lib.fa_kv4_read.argtypes = [_vp] * 9 + [_ci] * 6 + [_vp]
+lib.fa_decode_kv4_workspace_bytes.restype = _sz
+lib.fa_decode_kv4_workspace_bytes.argtypes = [_ci] * 6
+lib.fa_decode_kv4.argtypes = [_vp] * 10 + [_ci] * 5 + [_cf, _vp, _sz, _vp]
+_i32 = torch.int32
+
+
+def _args(where: str, stream, *tensors):
+    """The stream's handle and the tensors' addresses (None for None) for a call of the
+    cache operators; `tensors` are (name, tensor, dtype, shape).  The checks are those of
+    _need, and that the tensors (and a given stream) belong to the current device, where
+    the kernels are launched.  These calls run once per decoded token and layer, so the
+    checks that pass cost little; one that fails is explained by _need."""
+    dev = torch.cuda.current_device()
+    ptrs = []
+    for name, t, dtype, shape in tensors:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            _need(where, **{name: (t, dtype, shape)})
+            raise FAError(FA_ERR_INVALID_ARG, f"{where}({name}: on {t.device}, the current device is cuda:{dev})")
+        ptrs.append(t.data_ptr())
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev), ptrs
+    if stream.device_index != dev:
+        raise FAError(FA_ERR_INVALID_ARG, f"{where}(stream: of cuda:{stream.device_index}, the current device is cuda:{dev})")
+    return stream.cuda_stream, ptrs
+
+
+def _required(where: str, **tensors) -> None:
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise FAError(FA_ERR_INVALID_ARG, f"{where}({name}: expected a CUDA tensor, got {type(t).__name__})")
+
+
+def _cache_dims(where: str, kc):
+    if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
+        raise FAError(FA_ERR_INVALID_ARG, f"{where}(kc: expected uint8 [B, H_kv, C, d / 2])")
+    B, Hkv, C, half = kc.shape
+    return B, Hkv, C, 2 * half
+
+
+def fa_key_weights_workspace_bytes(B: int, H: int, H_kv: int, N: int, d: int, window: int) -> int:
+    return int(lib.fa_key_weights_workspace_bytes(B, H, H_kv, N, d, window))
+
+
+def fa_key_weights(q, k, lse, w, causal: bool, scale: float, workspace, window=None, n_rows=None,
+                   stream=None) -> None:
+    """Attention weight that each key of a prompt received from the last `window` queries
+    (None: all): w (fp32 [B, H_kv, >= N]) columns 0 .. N-1; lse is the forward's; n_rows:
+    int32 [B] tokens of each sequence, or None."""
+    _required("fa_key_weights", q=q, k=k, lse=lse, w=w, workspace=workspace)
+    B, H, N, d = _dims(q)
+    Hkv = k.shape[1] if k.dim() == 4 else -1
+    ldw = w.shape[-1] if w.dim() == 3 else -1
+    s, p = _args("fa_key_weights", stream, ("q", q, _bf, (B, H, N, d)), ("k", k, _bf, (B, Hkv, N, d)),
+                 ("lse", lse, _f32, (B, H, N)), ("w", w, _f32, (B, Hkv, ldw)), ("n_rows", n_rows, _i32, (B,)),
+                 ("workspace", workspace, _u8, (workspace.numel(),)))
+    _check(lib.fa_key_weights(*p[:5], B, H, Hkv, N, ldw, d, int(causal), N if window is None else int(window),
+                              float(scale), p[5], workspace.numel(), s), "fa_key_weights")
+
+
+def fa_evict_keep(w, idx, count, n_recent: int, n_sink: int, lens=None, stream=None) -> None:
+    """The idx.shape[-1] rows of each head that stay, by weight: idx (int32 [B, H_kv, keep],
+    ascending, -1 behind), count (int32 [B, H_kv]); w: fp32 [B, H_kv, C]; lens: int32 [B, H_kv]
+    rows in use, or None (C)."""
+    _required("fa_evict_keep", w=w, idx=idx, count=count)
+    if w.dim() != 3 or idx.dim() != 3:
+        raise FAError(FA_ERR_INVALID_ARG, "fa_evict_keep(w: expected [B, H_kv, C], idx: [B, H_kv, keep])")
+    B, Hkv, C = w.shape
+    keep = idx.shape[2]
+    s, p = _args("fa_evict_keep", stream, ("w", w, _f32, (B, Hkv, C)), ("lens", lens, _i32, (B, Hkv)),
+                 ("idx", idx, _i32, (B, Hkv, keep)), ("count", count, _i32, (B, Hkv)))
+    _check(lib.fa_evict_keep(*p, B, Hkv, C, keep, int(n_recent), int(n_sink), s), "fa_evict_keep")
+
+
+def fa_evict_slots(acc, pos, lens, seen, slots, budget: int, n_recent: int, n_sink: int, stream=None) -> None:
+    """The rows that slots.shape[-1] new tokens take in each head: free rows, then the lightest
+    of the rows in use; lens is updated.  acc: fp32, pos: int32 [B, H_kv, C]; lens: int32
+    [B, H_kv]; seen: int32 [B] tokens seen so far; slots: int32 [B, H_kv, T]."""
+    _required("fa_evict_slots", acc=acc, pos=pos, lens=lens, seen=seen, slots=slots)
+    if acc.dim() != 3 or slots.dim() != 3:
+        raise FAError(FA_ERR_INVALID_ARG, "fa_evict_slots(acc: expected [B, H_kv, C], slots: [B, H_kv, T])")
+    B, Hkv, C = acc.shape
+    T = slots.shape[2]
+    s, p = _args("fa_evict_slots", stream, ("acc", acc, _f32, (B, Hkv, C)), ("pos", pos, _i32, (B, Hkv, C)),
+                 ("lens", lens, _i32, (B, Hkv)), ("seen", seen, _i32, (B,)), ("slots", slots, _i32, (B, Hkv, T)))
+    _check(lib.fa_evict_slots(*p, B, Hkv, C, int(budget), T, int(n_recent), int(n_sink), s), "fa_evict_slots")
+
+
+def fa_kv4_append(k, v, kc, ks, vc, vs, signs=None, rows=None, slots=None, start=None, n_new=None, w=None, acc=None,
+                  pos=None, base=None, stream=None) -> None:
+    """Quantises rows of k, v (bf16 [B, H_kv, N, d]) into the cache (kc, vc: uint8
+    [B, H_kv, C, d / 2]; ks, vs: bf16 [B, H_kv, C]): source rows `rows` (int32 [B, H_kv, T], None:
+    0 .. N-1) to cache rows `slots` (int32 [B, H_kv, T]) or start + t (int32 [B, H_kv], None: 0)."""
+    where = "fa_kv4_append"
+    _required(where, k=k, v=v, ks=ks, vc=vc, vs=vs)
+    B, Hkv, C, d = _cache_dims(where, kc)
+    N = k.shape[2] if k.dim() == 4 else -1
+    for given in (rows, slots):
+        if given is not None and (not isinstance(given, torch.Tensor) or given.dim() != 3):
+            raise FAError(FA_ERR_INVALID_ARG, f"{where}(rows, slots: expected int32 [B, H_kv, T])")
+    T = rows.shape[2] if rows is not None else slots.shape[2] if slots is not None else N
+    ldw = w.shape[-1] if isinstance(w, torch.Tensor) and w.dim() == 3 else 0
+    s, p = _args(where, stream, ("k", k, _bf, (B, Hkv, N, d)), ("v", v, _bf, (B, Hkv, N, d)),
+                 ("signs", signs, _f32, (d,)), ("w", w, _f32, (B, Hkv, ldw)), ("rows", rows, _i32, (B, Hkv, T)),
+                 ("slots", slots, _i32, (B, Hkv, T)), ("start", start, _i32, (B, Hkv)), ("n_new", n_new, _i32, (B, Hkv)),
+                 ("base", base, _i32, (B,)), ("kc", kc, _u8, (B, Hkv, C, d // 2)), ("ks", ks, _bf, (B, Hkv, C)),
+                 ("vc", vc, _u8, (B, Hkv, C, d // 2)), ("vs", vs, _bf, (B, Hkv, C)), ("acc", acc, _f32, (B, Hkv, C)),
+                 ("pos", pos, _i32, (B, Hkv, C)))
+    _check(lib.fa_kv4_append(*p, B, Hkv, N, T, C, ldw, d, s), where)
+
+
+def fa_kv4_read(kc, ks, vc, vs, k, v, signs=None, slots=None, first: int = 0, lens=None, stream=None) -> None:
+    """The values that cache rows `slots` (int32 [B, H_kv, T]), or first + t, stand for: k, v
+    (bf16 [B, H_kv, T, d]); zeros for rows outside 0 .. lens-1."""
+    where = "fa_kv4_read"
+    _required(where, ks=ks, vc=vc, vs=vs, k=k, v=v)
+    B, Hkv, C, d = _cache_dims(where, kc)
+    T = k.shape[2] if k.dim() == 4 else -1
+    s, p = _args(where, stream, ("kc", kc, _u8, (B, Hkv, C, d // 2)), ("ks", ks, _bf, (B, Hkv, C)),
+                 ("vc", vc, _u8, (B, Hkv, C, d // 2)), ("vs", vs, _bf, (B, Hkv, C)), ("signs", signs, _f32, (d,)),
+                 ("slots", slots, _i32, (B, Hkv, T)), ("lens", lens, _i32, (B, Hkv)), ("k", k, _bf, (B, Hkv, T, d)),
+                 ("v", v, _bf, (B, Hkv, T, d)))
+    _check(lib.fa_kv4_read(*p, B, Hkv, T, C, int(first), d, s), where)
+
+
+def fa_decode_kv4_workspace_bytes(B: int, H: int, H_kv: int, C: int, d: int, weights: bool) -> int:
+    return int(lib.fa_decode_kv4_workspace_bytes(B, H, H_kv, C, d, int(weights)))
+
+
+def fa_decode_kv4(q, kc, ks, vc, vs, lens, o, lse, scale: float, workspace, signs=None, acc=None,
+                  stream=None) -> None:
+    """One decoding step over a 4-bit cache: q, o: bf16 [B, H, d]; lse: fp32 [B, H]; lens: int32
+    [B, H_kv]; acc (fp32 [B, H_kv, C] or None) gets each row's softmax weight added."""
+    where = "fa_decode_kv4"
+    _required(where, q=q, ks=ks, vc=vc, vs=vs, lens=lens, o=o, lse=lse, workspace=workspace)
+    B, Hkv, C, d = _cache_dims(where, kc)
+    H = q.shape[1] if q.dim() == 3 else -1
+    n_ws = workspace.numel()
+    s, p = _args(where, stream, ("q", q, _bf, (B, H, d)), ("kc", kc, _u8, (B, Hkv, C, d // 2)),
+                 ("ks", ks, _bf, (B, Hkv, C)), ("vc", vc, _u8, (B, Hkv, C, d // 2)), ("vs", vs, _bf, (B, Hkv, C)),
+                 ("signs", signs, _f32, (d,)), ("lens", lens, _i32, (B, Hkv)), ("o", o, _bf, (B, H, d)),
+                 ("lse", lse, _f32, (B, H)), ("acc", acc, _f32, (B, Hkv, C)), ("workspace", workspace, _u8, (n_ws,)))
+    _check(lib.fa_decode_kv4(*p[:10], B, H, Hkv, C, d, float(scale), p[10], n_ws, s), where)

@@ -210,6 +210,88 @@ int fa_fwd_fp8_gqa(const void* q8, const void* k8, const void* v8, const float* 
                    const float* sv, void* o, float* lse, int B, int H, int H_kv, int N, int d, int causal, float scale,
                    float S, int kv_order, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A key/value cache held in 4 bits, with eviction by accumulated attention weight
+ * ("FlashAttention (IT)", "Soluzioni specializzate": decoding against a cache; FP8's
+ * incoherent processing, "flash-attention-trading-models", "FA3", item 3, in 4 bits).
+ *
+ * A cache holds C rows (tokens) per (b, key/value head); C is a multiple of 128.
+ *   kc, vc: uint8 [B,H_kv,C,d/2] codes; ks, vs: bf16 [B,H_kv,C] scales.
+ * A row x of d values is stored as y = H diag(signs) x for keys when signs is given (H the
+ * unnormalised Sylvester Walsh-Hadamard matrix, signs d values +-1 in fp32), else y = x;
+ * s = bf16(max|y| / 7), c = min(7, max(-7, rint(y / s))), code c + 8, element 2i in the low
+ * nibble of byte i and element 2i + 1 in the high one.  Where s is 0 the codes are those of
+ * zeros; a row with an infinity or a NaN (in y) gets a NaN scale and reads as NaN.
+ * Beside it, per row: acc, fp32 [B,H_kv,C], the attention weight it has received, and pos,
+ * int32 [B,H_kv,C], its token's position.  lens, int32 [B,H_kv]: rows in use per head (values
+ * outside 0..C are read as the nearest of the two).  Rows in use are rows 0 .. lens-1, in any
+ * order of positions.  Memory behind them is never written by these calls, and what it holds
+ * never reaches a result.  All the int32 and fp32 arrays are device memory, read when the
+ * kernel runs, so that a captured graph follows them.
+ * Alignment: kc, ks, vc, vs, acc, pos, q, k, v, o 16 bytes, workspaces 256, others 4.
+ * Limits: C <= 2^30, d in {64, 128, 256}, and the limits above with C (and N, T) for N.
+ * ------------------------------------------------------------------------- */
+
+/* Attention weight received by each key of a prompt: w[b,hk,j] = the sum, over the query heads
+ * that share key/value head hk and over the query rows i of the window (i >= j if causal), of
+ * exp(scale q_i . k_j - lse_i).  q: bf16 [B,H,N,d], k: bf16 [B,H_kv,N,d], lse: fp32 [B,H,N] as
+ * fa_fwd / fa_fwd_gqa give it (read in the window only).
+ * n_rows: int32 [B] or NULL: tokens of each sequence (N); rows behind them neither give nor
+ * get weight (their w is 0).  The window is the last `window` rows of each sequence (window >= N:
+ * all of them).  w: fp32 [B,H_kv,ldw], ldw >= N; columns 0 .. N-1 are overwritten.
+ * workspace: >= fa_key_weights_workspace_bytes(). */
+size_t fa_key_weights_workspace_bytes(int B, int H, int H_kv, int N, int d, int window);
+int fa_key_weights(const void* q, const void* k, const float* lse, float* w, const int* n_rows, int B, int H, int H_kv,
+                   int N, int ldw, int d, int causal, int window, float scale, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* Eviction at the end of a prompt: of rows 0 .. len-1 (len = lens[b,hk], or C when lens is NULL)
+ * the `keep` rows that stay: the first n_sink and the last n_recent rows, then those with the
+ * largest w (fp32 [B,H_kv,C], any C), the lowest row first among equals.  idx: int32
+ * [B,H_kv,keep], the rows in ascending order, -1 behind them; count: int32 [B,H_kv],
+ * min(len, keep).  n_sink + n_recent <= keep.  -0 equals 0; a NaN counts as the largest weight. */
+int fa_evict_keep(const float* w, const int* lens, int* idx, int* count, int B, int H_kv, int C, int keep, int n_recent,
+                  int n_sink, void* stream);
+
+/* Eviction while decoding: the rows of a cache that T new tokens take, of the first `budget`
+ * rows (budget <= C): free rows (lens, lens + 1, ...) while there are some, then the rows in use
+ * with the smallest acc, in ascending order, the highest row first where equal ones have to be
+ * chosen among.  Rows with pos < n_sink or pos >= seen[b] - n_recent go last.  T <= budget.
+ * slots: int32 [B,H_kv,T]; lens is updated to min(budget, lens + T).  Nothing else changes:
+ * fa_kv4_append with these slots writes the new rows. */
+int fa_evict_slots(const float* acc, const int* pos, int* lens, const int* seen, int* slots, int B, int H_kv, int C,
+                   int budget, int T, int n_recent, int n_sink, void* stream);
+
+/* Writes T rows of each head into the cache.  k, v: bf16 [B,H_kv,N,d].  Row t of a head comes
+ * from source row rows[b,hk,t] (int32 [B,H_kv,T]; NULL: row t, T <= N) and goes to cache row
+ * slots[b,hk,t] (int32 [B,H_kv,T]), or to start[b,hk] + t (int32 [B,H_kv]; NULL: 0); not both
+ * slots and start.  Only the first n_new[b,hk] are written (int32 [B,H_kv]; NULL: T), and none
+ * whose source row is outside 0 .. N-1 or whose cache row is outside 0 .. C-1.  Cache rows of one
+ * head must differ from each other (of rows given twice, what is left is undefined).
+ * acc (or NULL): the rows' weight becomes w[b,hk,source row] (fp32 [B,H_kv,ldw], ldw >= N; NULL:
+ * 0).  pos (or NULL): it becomes base[b] + source row (int32 [B]; NULL: 0).
+ * lens is the caller's: add what was appended. */
+int fa_kv4_append(const void* k, const void* v, const float* signs, const float* w, const int* rows, const int* slots,
+                  const int* start, const int* n_new, const int* base, void* kc, void* ks, void* vc, void* vs,
+                  float* acc, int* pos, int B, int H_kv, int N, int T, int C, int ldw, int d, void* stream);
+
+/* The values that cache rows stand for, as bf16 k, v [B,H_kv,T,d] in the original basis: rows
+ * slots[b,hk,t], or first + t (slots NULL); zeros where the row is outside 0 .. lens-1 (lens
+ * NULL: 0 .. C-1). */
+int fa_kv4_read(const void* kc, const void* ks, const void* vc, const void* vs, const float* signs, const int* slots,
+                const int* lens, void* k, void* v, int B, int H_kv, int T, int C, int first, int d, void* stream);
+
+/* fa_decode over a 4-bit cache with a length per head: q, o: bf16 [B,H,d]; lse: fp32 [B,H];
+ * query head h reads key/value head h / (H / H_kv), at most 16 query heads share one.  signs:
+ * as given to fa_kv4_append (the query is rotated inside).  A head with no rows gives o = 0 and
+ * lse = -inf.  acc (or NULL): acc[b,hk,j] += the sum over the query heads that share hk of
+ * their softmax weight of row j.  workspace: >= fa_decode_kv4_workspace_bytes(..., weights = acc
+ * given); its contents on entry do not matter.  Two launches on `stream`. */
+size_t fa_decode_kv4_workspace_bytes(int B, int H, int H_kv, int C, int d, int weights);
+int fa_decode_kv4(const void* q, const void* kc, const void* ks, const void* vc, const void* vs, const float* signs,
+                  const int* lens, void* o, float* lse, float* acc, int B, int H, int H_kv, int C, int d, float scale,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Human-readable name of an fa_status code. */
 const char* fa_status_string(int status);
 
