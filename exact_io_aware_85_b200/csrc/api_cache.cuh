@@ -21,14 +21,53 @@ int launched() {
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
-// Chunks per key/value head: one wave of CTAs.
-int kv4_splits(int B, int Hkv, int C) { return std::max(1, std::min(C / fa::kKv4Rows, 148 / (B * Hkv))); }
+// The decoding step's plan, from the sizes alone: one CTA per SM (148), fewer when the caches
+// hold fewer blocks; rows of the score buffer padded to an even number of heads.
+struct Kv4Plan {
+  int nt, gp, grid, slots;
+  size_t part_o, part_ml, first, scores, bytes;  // offsets in bytes
+};
 
-template <int D>
-void launch_kv4_decode(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
-  fa::fa_kv4_decode_kernel<D><<<dim3(a.nsplit, a.BHkv), 128, 0, s>>>(a);
+Kv4Plan kv4_plan(int B, int H, int Hkv, int C, int d, bool weights) {
+  Kv4Plan p;
+  const int g = H / Hkv;
+  const long long bhkv = static_cast<long long>(B) * Hkv;
+  p.nt = g > 8 ? 2 : 1;
+  p.gp = g == 1 ? 1 : (g + 1) / 2 * 2;
+  const int block = (p.nt == 1 && d <= 128 ? 16 : 8) * 32;
+  p.grid = static_cast<int>(std::min<long long>(148, bhkv * ((C + block - 1) / block)));
+  p.slots = static_cast<int>(p.grid + bhkv);
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  p.part_o = 0;
+  p.part_ml = p.part_o + up(static_cast<size_t>(p.slots) * 8 * p.nt * d * 4);
+  p.first = p.part_ml + up(static_cast<size_t>(p.slots) * 8 * p.nt * 8);
+  p.scores = p.first + up((static_cast<size_t>(bhkv) + 1) * 4);
+  p.bytes = p.scores + (weights ? up(static_cast<size_t>(bhkv) * C * p.gp * 4) : 0);
+  return p;
+}
+
+template <int D, int NT>
+int launch_kv4_decode(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
+  using L = fa::Kv4Cfg<D, NT>;
+  auto kern = fa::fa_kv4_decode_kernel<D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  if (e != cudaSuccess) return cuda_fail(e);
+  kern<<<a.grid, L::THREADS, L::BYTES, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  // the second kernel is launched while the first one runs and waits for it on the device
   const int chunk = 4096;
-  fa::fa_kv4_combine_kernel<D><<<dim3(a.acc ? (a.C + chunk - 1) / chunk : 1, a.BHkv), 256, 0, s>>>(a, chunk);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.acc ? (a.C + chunk - 1) / chunk : 1, a.BHkv);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, fa::fa_kv4_combine_kernel<D, NT>, a, chunk);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
 }  // namespace
@@ -201,9 +240,7 @@ int fa_kv4_read(const void* kc, const void* ks, const void* vc, const void* vs, 
 size_t fa_decode_kv4_workspace_bytes(int B, int H, int H_kv, int C, int d, int weights) {
   if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || check_cache(B, H_kv, C, d) != FA_OK) return 0;
   if (H / H_kv > 16 || static_cast<long long>(B) * H_kv > 65535) return 0;
-  size_t floats = static_cast<size_t>(kv4_splits(B, H_kv, C)) * B * H * (static_cast<size_t>(d) + 2);
-  if (weights) floats += static_cast<size_t>(B) * H * C;
-  return (floats * sizeof(float) + 255) / 256 * 256;
+  return kv4_plan(B, H, H_kv, C, d, weights != 0).bytes;
 }
 
 int fa_decode_kv4(const void* q, const void* kc, const void* ks, const void* vc, const void* vs, const float* signs,
@@ -235,16 +272,19 @@ int fa_decode_kv4(const void* q, const void* kc, const void* ks, const void* vc,
   a.C = C;
   a.BHkv = B * H_kv;
   a.g = H / H_kv;
-  a.nsplit = kv4_splits(B, H_kv, C);
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = a.part_o + static_cast<size_t>(a.nsplit) * B * H * d;
-  a.scores = acc ? a.part_ml + static_cast<size_t>(a.nsplit) * B * H * 2 : nullptr;
+  const Kv4Plan p = kv4_plan(B, H, H_kv, C, d, acc != nullptr);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.gp = p.gp;
+  a.grid = p.grid;
+  a.part_o = reinterpret_cast<float*>(ws + p.part_o);
+  a.part_ml = reinterpret_cast<float*>(ws + p.part_ml);
+  a.first = reinterpret_cast<int*>(ws + p.first);
+  a.scores = acc ? reinterpret_cast<float*>(ws + p.scores) : nullptr;
   a.scale_log2 = scale * 1.4426950408889634f / (signs ? static_cast<float>(d) : 1.f);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 64) launch_kv4_decode<64>(a, s);
-  else if (d == 128) launch_kv4_decode<128>(a, s);
-  else launch_kv4_decode<256>(a, s);
-  return launched();
+  if (d == 64) return p.nt == 1 ? launch_kv4_decode<64, 1>(a, s) : launch_kv4_decode<64, 2>(a, s);
+  if (d == 128) return p.nt == 1 ? launch_kv4_decode<128, 1>(a, s) : launch_kv4_decode<128, 2>(a, s);
+  return p.nt == 1 ? launch_kv4_decode<256, 1>(a, s) : launch_kv4_decode<256, 2>(a, s);
 }
 
 }  // extern "C"
