@@ -34,13 +34,13 @@ Kv4Plan kv4_plan(int B, int H, int Hkv, int C, int d, bool weights) {
   const long long bhkv = static_cast<long long>(B) * Hkv;
   p.nt = g > 8 ? 2 : 1;
   p.gp = g == 1 ? 1 : (g + 1) / 2 * 2;
-  const int block = (p.nt == 1 && d <= 128 ? 16 : 8) * 32;
+  const int block = fa::kv4_warps(d, p.nt) * 32;
   p.grid = static_cast<int>(std::min<long long>(148, bhkv * ((C + block - 1) / block)));
   p.slots = static_cast<int>(p.grid + bhkv);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   p.part_o = 0;
   p.part_ml = p.part_o + up(static_cast<size_t>(p.slots) * 8 * p.nt * d * 4);
-  p.first = p.part_ml + up(static_cast<size_t>(p.slots) * 8 * p.nt * 8);
+  p.first = p.part_ml + up(static_cast<size_t>(p.slots) * 8 * p.nt * 16);
   p.scores = p.first + up((static_cast<size_t>(bhkv) + 1) * 4);
   p.bytes = p.scores + (weights ? up(static_cast<size_t>(bhkv) * C * p.gp * 4) : 0);
   return p;
@@ -56,7 +56,7 @@ int launch_kv4_decode(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
   // the second kernel is launched while the first one runs and waits for it on the device
-  const int chunk = 4096;
+  const int chunk = 1024;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.acc ? (a.C + chunk - 1) / chunk : 1, a.BHkv);
   cfg.blockDim = dim3(256);

@@ -185,21 +185,27 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const Kv4ReadArgs a) {
 //
 //   * Warps work alone: a warp takes 32 keys at a time, holds their running maximum, sum and
 //     output for all query heads that share them, and meets the other warps only when the
-//     CTA's part of a head ends.  Its rows arrive by bulk copies through a ring of its own.
+//     CTA's part of a head ends.  Blocks of 32 keys a warp arrive by bulk copies through a ring.
 //   * Products are warp-level m16n8k16 MMAs with the codes on the 16-wide side and the query
 //     heads on the 8-wide one.  Which key is which row, and which element which column, is free
 //     as long as both operands agree, so every lane reads its codes from shared memory as whole
 //     words and unpacks them in place: for K the pairs of a word are consecutive k entries; for
 //     V the same element of two keys is, and the eight elements of a word belong to eight MMAs.
-//   * Unpacking: (w & 0xf000f) | 0x6400_6400 is the fp16 pair 1024 + code, and the nibbles at
-//     bits 4-7 read 1024 + 16 code, so one shift serves four pairs; one packed add or fma leaves
-//     the code itself, exact.  V's codes go to bf16 (128 + code), beside P times the row's scale,
-//     which needs the exponent range.
+//   * Unpacking is one AND for two codes: w & 0xf000f is a pair of fp16 subnormals, n 2^-24 for
+//     the nibbles n = c + 8, and w & 0xf000f0 is n 2^-20, exact in the MMA; one shift by 8 serves
+//     the other half of the word.  The factor 16 goes into q (for K) or into the result (for V).
+//     The 8 leaves K's products through the accumulator's start, -8 sum(q), and V's through one
+//     more MMA whose codes are all 8: it gathers 8 sum(P), which is taken off at the end.
+//     (fp16 1024 + n and an addition instead: 594 instead of about 400 instructions per 32 keys
+//     of d = 128, and the same in bf16 for V.)
 //   * q in fp16, scaled by a power of two per head so that its largest element is near 2^14: a
-//     bf16 query is exact; a rotated query is held as a sum of two fp16 numbers (22 bits).  With at most four
-//     heads the second number sits in the MMA's unused columns.
-//   * Work is one list of blocks (32 keys a warp) over all heads' lengths, cut into equal parts,
-//     one per CTA: ragged batches fill the GPU evenly.
+//     bf16 query is exact; a rotated query is held as a sum of two fp16 numbers (22 bits).  With
+//     at most four heads the second number sits in the MMA's unused columns.
+//   * P times the row's scale, u = p vs, meets V's codes in fp16 too (11 bits, so its rounding
+//     stays below that of the bf16 output).  Its range: u is held relative to 2^R, a running
+//     maximum of u like m of the scores, so what flushes is 2^-24 of the largest.
+//   * Work is one list of blocks over all heads' lengths, cut into equal parts, one per CTA:
+//     ragged batches fill the GPU evenly.
 struct Kv4DecodeArgs {
   const __nv_bfloat16* q;  // [B*H, d]
   const float* signs;      // [d] or null
@@ -212,7 +218,7 @@ struct Kv4DecodeArgs {
   float* lse;              // [B*H]
   float* acc;              // [B*Hkv, C] or null
   float* part_o;           // [grid + B*Hkv, 8 NT d]: slot (CTA + head), in the merge's fragment order
-  float* part_ml;          // [grid + B*Hkv, 8 NT, 2]
+  float* part_ml;          // [grid + B*Hkv, 8 NT, 4]: m, l, R
   int* first;              // [B*Hkv + 1]: blocks before each head
   float* scores;           // [B*Hkv, C, gp] in log2 units, or null
   int C, BHkv, g, gp, grid;
@@ -223,55 +229,35 @@ __device__ __forceinline__ int kv4_len(const int* lens, int bh, int C) { return 
 
 constexpr float kKv4Lowest = -3.0e38f;  // the running maximum before the first key
 
+// Working warps per CTA; one more loads.  As many as the registers of the output and the codes
+// leave room for: 128, 168 or 255 a thread.
+__host__ __device__ constexpr int kv4_warps(int d, int nt) { return nt == 1 && d <= 128 ? 15 : nt * d <= 256 ? 11 : 7; }
+
 template <int D, int NT>
 struct Kv4Cfg {
-  static constexpr int NW = (NT == 1 && D <= 128) ? 16 : 8;  // warps: 128 or 255 registers a thread
-  static constexpr int THREADS = NW * 32;
+  static constexpr int NW = kv4_warps(D, NT);
+  static constexpr int THREADS = NW * 32 + 32;
   static constexpr int BLOCK = NW * 32;                      // keys per block
   static constexpr int ROW = D / 2;                          // bytes of codes per row
-  static constexpr int STAGE = 2 * 32 * ROW + 128;           // K, V codes and scales of 32 rows
-  static constexpr int STAGES = 200 * 1024 / (NW * STAGE);
+  static constexpr int OFF_V = BLOCK * ROW;
+  static constexpr int OFF_KS = 2 * BLOCK * ROW, OFF_VS = OFF_KS + 2 * BLOCK;
+  static constexpr int STAGE = OFF_VS + 2 * BLOCK;
+  static constexpr int STAGES = 204 * 1024 / STAGE;
   static constexpr int KSTEPS = D / 16;
   static constexpr int MT = D / 16;                          // 16-row tiles of O^T
-  static constexpr int MC = 4;                               // ... merged at a time
-  static constexpr int OFF_Q = NW * STAGES * STAGE;          // fp16 B fragments: [NT][2][KSTEPS][32] x 8 bytes
+  static constexpr int MC = 2;                               // ... merged at a time
+  static constexpr int OFF_Q = STAGES * STAGE;               // fp16 B fragments: [NT][2][KSTEPS][32] x 8 bytes
   static constexpr int OFF_RED = OFF_Q;                      // the merge's buffer lies over them
   static constexpr int Q_BYTES = NT * 2 * KSTEPS * 32 * 8;
-  static constexpr int RED_BYTES = NW * NT * 32 * 16;        // one 16-row tile of every warp
-  static constexpr int OFF_ML = OFF_Q + (Q_BYTES > RED_BYTES ? Q_BYTES : RED_BYTES);  // [2][NW][8 NT]
-  static constexpr int OFF_FAC = OFF_ML + 2 * NW * 8 * NT * 4;  // [8 NT]
-  static constexpr int OFF_BAR = OFF_FAC + 8 * NT * 4;
-  static constexpr int OFF_MISC = OFF_BAR + NW * STAGES * 8;
+  static constexpr int RED_BYTES = NW * MC * NT * 32 * 16;
+  static constexpr int OFF_ML = OFF_Q + (Q_BYTES > RED_BYTES ? Q_BYTES : RED_BYTES);  // [3][NW][8 NT]
+  static constexpr int OFF_FAC = OFF_ML + 3 * NW * 8 * NT * 4;  // [2][8 NT]
+  static constexpr int OFF_BAR = OFF_FAC + 2 * 8 * NT * 4;
+  static constexpr int OFF_MISC = OFF_BAR + 2 * STAGES * 8;
   static constexpr int BYTES = OFF_MISC + 256;
   static_assert(STAGES >= 2 && BYTES <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-// the fp16 pairs (e0, e4), (e1, e5), (e2, e6), (e3, e7) of the eight codes in w, less 8
-__device__ __forceinline__ void kv4_unpack_f16(uint32_t w, uint32_t (&r)[4]) {
-  const uint32_t w8 = w >> 8;
-  const uint32_t magic = 0x64006400u, off = 0xE408E408u /* -1032 */, s16 = 0x2C002C00u /* 1/16 */, o16 = 0xD480D480u /* -72 */;
-  uint32_t x;
-  x = and_or(w, 0x000f000fu, magic);
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r[0]) : "r"(x), "r"(off));
-  x = and_or(w, 0x00f000f0u, magic);
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[1]) : "r"(x), "r"(s16), "r"(o16));
-  x = and_or(w8, 0x000f000fu, magic);
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r[2]) : "r"(x), "r"(off));
-  x = and_or(w8, 0x00f000f0u, magic);
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[3]) : "r"(x), "r"(s16), "r"(o16));
-}
-// the bf16 pair of code i (0..3) of each half of t, less 8
-__device__ __forceinline__ uint32_t kv4_unpack_bf16(uint32_t t, int i) {
-  const uint32_t x = and_or(t >> (4 * i), 0x000f000fu, 0x43004300u);
-  uint32_t r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0xC308C308u) /* -136 */);
-  return r;
-}
 __device__ __forceinline__ void mma_16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -285,6 +271,11 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ float bf16_bits_to_float(unsigned short u) {
   return __uint_as_float(static_cast<uint32_t>(u) << 16);
 }
@@ -297,21 +288,25 @@ struct Kv4Cursor {
 template <int D, int NT>
 __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kernel(const Kv4DecodeArgs a) {
   using L = Kv4Cfg<D, NT>;
-  constexpr int NW = L::NW, ST = L::STAGES, NQ = 8 * NT;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* const smem = smem_raw;
+  constexpr int NW = L::NW, ST = L::STAGES, NQ = 8 * NT, WORKERS = NW * 32;
+  extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grp = lane >> 2, tq = lane & 3;
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR) + warp * ST;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* const empty = full + ST;
   volatile int* const abort_sh = reinterpret_cast<volatile int*>(smem + L::OFF_MISC);
-  int* const scan = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);  // [NW + 4]
-  float* const fac_sh = reinterpret_cast<float*>(smem + L::OFF_FAC);
-  float* const wm = reinterpret_cast<float*>(smem + L::OFF_ML);  // [NW][NQ]
+  int* const scan = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);  // [NW + 1 + 2]
+  float* const fac_sh = reinterpret_cast<float*>(smem + L::OFF_FAC);  // [NQ] factors, [NQ] accumulator starts
+  float* const wm = reinterpret_cast<float*>(smem + L::OFF_ML);       // [NW][NQ] each
   float* const wl = wm + NW * NQ;
+  float* const wr = wl + NW * NQ;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (tid == 0) *abort_sh = 0;
-  if (lane == 0) {
-    for (int s = 0; s < ST; ++s) mbar_init(&bars[s], 1);
+  if (tid == 0) {
+    *abort_sh = 0;
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], NW);
+    }
     fence_mbar_init();
   }
   // ---- this CTA's part of the list of blocks -------------------------------------------
@@ -329,7 +324,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
   int before = incl - mine, total = 0;
-  for (int w = 0; w < NW; ++w) {
+  for (int w = 0; w < NW + 1; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
@@ -345,7 +340,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
     if (tid == 0) a.first[a.BHkv] = total;
   }
   if (u0 >= u1) return;
-  int* const start = scan + NW;
+  int* const start = scan + NW + 1;
   if (u0 >= before && u0 < before + mine) {
     int f = before, h = h0;
     while (true) {
@@ -358,63 +353,65 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
     start[1] = u0 - f;
   }
   __syncthreads();
-  Kv4Cursor cur, nxt;
+  Kv4Cursor cur;
   cur.bh = start[0];
   cur.blk = start[1];
   cur.len = kv4_len(a.lens, cur.bh, a.C);
   cur.nblk = nblocks(cur.len);
-  nxt = cur;
-  int left = u1 - u0, ahead = u1 - u0;  // blocks to work on, blocks to load
-  auto step = [&](Kv4Cursor& c, int& n) {
-    --n;
-    if (++c.blk == c.nblk && n > 0) {
-      c.blk = 0;
-      do {
-        c.len = kv4_len(a.lens, ++c.bh, a.C);
-        c.nblk = nblocks(c.len);
-      } while (c.nblk == 0);
-    }
+  int left = u1 - u0;  // blocks to go
+  auto next_head = [&]() {
+    cur.blk = 0;
+    do {
+      cur.len = kv4_len(a.lens, ++cur.bh, a.C);
+      cur.nblk = nblocks(cur.len);
+    } while (cur.nblk == 0);
   };
-  uint8_t* const ring = smem + warp * ST * L::STAGE;
-  int put = 0, got = 0;  // copies started, copies waited for
-  // starts the copies of this warp's next block that has keys; every lane follows
-  auto load_next = [&]() {
-    while (ahead > 0) {
-      const int key0 = nxt.blk * L::BLOCK + warp * 32;
-      const bool some = key0 < nxt.len;
-      if (some && lane == 0) {
-        uint8_t* st = ring + (put % ST) * L::STAGE;
-        uint64_t* bar = &bars[put % ST];
-        const size_t row = static_cast<size_t>(nxt.bh) * a.C + key0;
-        mbar_arrive_expect_tx(bar, L::STAGE);
-        bulk_load(st, a.kc + row * L::ROW, 32 * L::ROW, bar);
-        bulk_load(st + 64 * L::ROW, a.ks + row, 64, bar);
-        bulk_load(st + 32 * L::ROW, a.vc + row * L::ROW, 32 * L::ROW, bar);
-        bulk_load(st + 64 * L::ROW + 64, a.vs + row, 64, bar);
+
+  if (warp == NW) {
+    // ================= the loading warp: one thread, block after block ======================
+    if (lane == 0) {
+      int t = 0;
+      while (true) {
+        const int s = t % ST;
+        if (!mbar_wait(&empty[s], ((t / ST) & 1) ^ 1, abort_sh, 31)) break;
+        const int key0 = cur.blk * L::BLOCK;
+        const int rows = min(L::BLOCK, (cur.len - key0 + 31) & ~31);  // whole 32-row chunks: inside the capacity
+        uint8_t* st = smem + s * L::STAGE;
+        const size_t row = static_cast<size_t>(cur.bh) * a.C + key0;
+        mbar_arrive_expect_tx(&full[s], rows * (2 * L::ROW + 4));
+        bulk_load(st, a.kc + row * L::ROW, rows * L::ROW, &full[s]);
+        bulk_load(st + L::OFF_KS, a.ks + row, rows * 2, &full[s]);
+        bulk_load(st + L::OFF_V, a.vc + row * L::ROW, rows * L::ROW, &full[s]);
+        bulk_load(st + L::OFF_VS, a.vs + row, rows * 2, &full[s]);
+        ++t;
+        if (--left == 0) break;
+        if (++cur.blk == cur.nblk) next_head();
       }
-      step(nxt, ahead);
-      if (some) {
-        ++put;
-        return;
-      }
+      // every copy has landed before the block ends
+      for (int i = max(0, t - ST); i < t; ++i) mbar_wait_drain(&full[i % ST], (i / ST) & 1, 100000000ull);
     }
-  };
-#pragma unroll 1
-  for (int s = 0; s < ST; ++s) load_next();
+    return;
+  }
 
   const int g = a.g;
   const bool rotated = a.signs != nullptr;
   const bool dup = NT == 1 && rotated && g <= 4;  // second halves of q in columns 4-7
   const bool two = rotated && !dup;
+  constexpr int EPL = D / 4 < 32 ? D / 4 : 32;    // elements of a lane's chunk of a key
+  constexpr float kTwo24 = 16777216.f;
   bool ok = true;
+  int t = 0;  // blocks taken from the ring
+  // row r of a 16-key tile is key r ^ ((r >> 1) & 1): the rows that one load touches then
+  // alternate between the two halves of a 128-byte line
+  const int kr = grp ^ ((grp >> 1) & 1);
 
   while (left > 0) {
     // ================= one head: q into fragments =======================================
     const int bh = cur.bh;
     __half* const qf = reinterpret_cast<__half*>(smem + L::OFF_Q);
-    constexpr int EPL = D / 4 < 32 ? D / 4 : 32;  // elements of a lane's chunk of a key
-    for (int i = tid; i < L::Q_BYTES / 16; i += L::THREADS) reinterpret_cast<uint4*>(qf)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+    for (int i = tid; i < L::Q_BYTES / 16; i += WORKERS) reinterpret_cast<uint4*>(qf)[i] = make_uint4(0, 0, 0, 0);
+    for (int n = tid; n < 2 * NQ; n += WORKERS) fac_sh[n] = 0.f;
+    named_bar_sync(1, WORKERS);
     for (int n = warp; n < g; n += NW) {
       constexpr int E = D / 32;
       const __nv_bfloat16* qrow = a.q + (static_cast<size_t>(bh) * g + n) * D + lane * E;
@@ -445,18 +442,20 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
 #pragma unroll
       for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
       top = __reduce_max_sync(0xffffffffu, top);
-      // 2^k with |q| 2^k < 2^15; a query that is not finite goes through as it is
-      int k = 14 - (static_cast<int>(top >> 23) - 127);
-      if (top >= 0x7f800000u) k = 0;
-      k = min(k, 126);  // 2^k and 2^-k stay normal
+      // 2^k with |q| 2^k < 2^15 (a query that is not finite, or past 2^110, goes on as infinities)
+      const int k = max(-95, min(14 - (static_cast<int>(top >> 23) - 127), 120));
       const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+      float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const float x = y[i] * up;
-        const __half hi = __float2half_rn(x);
-        const __half lo = __float2half_rn(x - __half2float(hi));
         const int j = lane * E + i;
         const int c = j / (4 * EPL), r = j % (4 * EPL), e = r & 7;
+        // odd elements meet the nibbles at bits 4-7, which count 16 times
+        const float x = (e & 1) ? y[i] * up * 0.0625f : y[i] * up;
+        const __half hi = __float2half_rn(x);
+        const __half lo = __float2half_rn(x - __half2float(hi));
+        const float back = rotated ? __half2float(hi) + __half2float(lo) : __half2float(hi);
+        sum += (e & 1) ? back * 16.f : back;
         const int ks = c * (EPL / 4) + ((r % EPL) >> 3) * 2 + ((e & 3) >> 1);
         const int sub = (e & 1) * 2 + (e >> 2), ql = r / EPL;
         const int nt = n >> 3, col = n & 7;
@@ -466,227 +465,257 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
           else qf[((((nt * 2 + 1) * L::KSTEPS + ks) * 32 + col * 4 + ql) << 2) + sub] = lo;
         }
       }
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       if (lane == 0) {
-        const float f = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+        const float f = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 24 - k) << 23);
         fac_sh[n] = f;
         if (dup) fac_sh[n + 4] = f;
+        fac_sh[NQ + n] = sum * (-8.f / kTwo24);
       }
     }
-    for (int n = tid; n < NQ; n += L::THREADS)
-      if (n >= g && !(dup && n >= 4 && n < 4 + g)) fac_sh[n] = 0.f;
-    __syncthreads();
-    float fac[NT][2], m_run[NT][2], l_run[NT][2], oacc[NT][L::MT][4];
+    named_bar_sync(1, WORKERS);
+    float fac[NT][2], x0[NT][2], m_run[NT][2], r_run[NT][2], kq[NT][2], l_run[NT][2], oacc[NT][L::MT][4], ones[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         fac[j][c] = fac_sh[8 * j + 2 * tq + c];
-        m_run[j][c] = kKv4Lowest;
+        x0[j][c] = fac_sh[NQ + 8 * j + 2 * tq + c];
+        m_run[j][c] = r_run[j][c] = kKv4Lowest;
+        kq[j][c] = 1.f;
         l_run[j][c] = 0.f;
+        ones[j][c] = ones[j][c + 2] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < L::MT; ++i) oacc[j][i][0] = oacc[j][i][1] = oacc[j][i][2] = oacc[j][i][3] = 0.f;
     }
     const uint2* const qfrag = reinterpret_cast<const uint2*>(qf) + lane;
     // ================= the head's blocks =================================================
-    do {
-      const int key0 = cur.blk * L::BLOCK + warp * 32;
+    const int end = min(cur.nblk, cur.blk + left);
+    left -= end - cur.blk;
+    for (int blk = cur.blk; blk < end; ++blk, ++t) {
+      const int s = t % ST;
+      const uint8_t* const st = smem + s * L::STAGE + warp * 32 * L::ROW;
+      const int key0 = blk * L::BLOCK + warp * 32;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[s], (t / ST) & 1, abort_sh, 30));
       if (ok && key0 < cur.len) {
-        const uint8_t* st = ring + (got % ST) * L::STAGE;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars[got % ST], (got / ST) & 1, abort_sh, 30));
-        ++got;
-        if (ok) {
-          // row r of a 16-key tile is key r ^ ((r >> 1) & 1): the rows that one load touches then
-          // alternate between the two halves of a 128-byte line
-          const int kr = grp ^ ((grp >> 1) & 1);
-          float x[2][NT][4];
+        float x[2][NT][4];
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) x[t][j][0] = x[t][j][1] = x[t][j][2] = x[t][j][3] = 0.f;
+          for (int j = 0; j < NT; ++j) {
+            x[u][j][0] = x[u][j][2] = x0[j][0];
+            x[u][j][1] = x[u][j][3] = x0[j][1];
+          }
 #pragma unroll
-          for (int c = 0; c < D / (4 * EPL); ++c) {
-            uint32_t w[4][EPL / 8];
+        for (int c = 0; c < D / (4 * EPL); ++c) {
+          uint32_t w[4][EPL / 8];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const uint8_t* p = st + (8 * r + kr) * L::ROW + c * 2 * EPL + tq * (EPL / 2);
-              if constexpr (EPL == 32) {
-                const uint4 v = *reinterpret_cast<const uint4*>(p);
-                w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
-              } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(p);
-                w[r][0] = v.x, w[r][1] = v.y;
-              }
+          for (int r = 0; r < 4; ++r) {
+            const uint8_t* p = st + (8 * r + kr) * L::ROW + c * 2 * EPL + tq * (EPL / 2);
+            if constexpr (EPL == 32) {
+              const uint4 v = *reinterpret_cast<const uint4*>(p);
+              w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(p);
+              w[r][0] = v.x, w[r][1] = v.y;
             }
+          }
 #pragma unroll
-            for (int i = 0; i < EPL / 8; ++i) {
-              uint32_t u[4][4];
+          for (int i = 0; i < EPL / 8; ++i)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) kv4_unpack_f16(w[r][i], u[r]);
+            for (int h = 0; h < 2; ++h) {
+              const int ks = c * (EPL / 4) + 2 * i + h;
+              uint32_t lo[4], hi[4];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int ks = c * (EPL / 4) + 2 * i + h;
+              for (int r = 0; r < 4; ++r) {
+                const uint32_t v = h ? w[r][i] >> 8 : w[r][i];
+                lo[r] = v & 0x000f000fu;
+                hi[r] = v & 0x00f000f0u;
+              }
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                  const uint2 b = qfrag[((j * 2) * L::KSTEPS + ks) * 32];
-                  mma_16816_f16(x[0][j], u[0][2 * h], u[1][2 * h], u[0][2 * h + 1], u[1][2 * h + 1], b.x, b.y);
-                  mma_16816_f16(x[1][j], u[2][2 * h], u[3][2 * h], u[2][2 * h + 1], u[3][2 * h + 1], b.x, b.y);
-                  if (two) {
-                    const uint2 b2 = qfrag[((j * 2 + 1) * L::KSTEPS + ks) * 32];
-                    mma_16816_f16(x[0][j], u[0][2 * h], u[1][2 * h], u[0][2 * h + 1], u[1][2 * h + 1], b2.x, b2.y);
-                    mma_16816_f16(x[1][j], u[2][2 * h], u[3][2 * h], u[2][2 * h + 1], u[3][2 * h + 1], b2.x, b2.y);
-                  }
+              for (int j = 0; j < NT; ++j) {
+                const uint2 b = qfrag[((j * 2) * L::KSTEPS + ks) * 32];
+                mma_16816_f16(x[0][j], lo[0], lo[1], hi[0], hi[1], b.x, b.y);
+                mma_16816_f16(x[1][j], lo[2], lo[3], hi[2], hi[3], b.x, b.y);
+                if (two) {
+                  const uint2 b2 = qfrag[((j * 2 + 1) * L::KSTEPS + ks) * 32];
+                  mma_16816_f16(x[0][j], lo[0], lo[1], hi[0], hi[1], b2.x, b2.y);
+                  mma_16816_f16(x[1][j], lo[2], lo[3], hi[2], hi[3], b2.x, b2.y);
                 }
               }
             }
+        }
+        float vs[4];
+        const unsigned short* const ksp =
+            reinterpret_cast<const unsigned short*>(smem + s * L::STAGE + L::OFF_KS) + warp * 32 + kr;
+        const bool tail = key0 + 32 > cur.len;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float ks = bf16_bits_to_float(ksp[8 * r]);
+          vs[r] = bf16_bits_to_float(ksp[L::BLOCK + 8 * r]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            float& xa = x[r >> 1][j][2 * (r & 1)];
+            float& xb = x[r >> 1][j][2 * (r & 1) + 1];
+            if (NT == 1 && dup) {
+              xa += __shfl_xor_sync(0xffffffffu, xa, 2);
+              xb += __shfl_xor_sync(0xffffffffu, xb, 2);
+            }
+            xa *= ks * fac[j][0];
+            xb *= ks * fac[j][1];
           }
-          float vs[4];
-          const unsigned short* const sc = reinterpret_cast<const unsigned short*>(st + 64 * L::ROW);
-          const bool tail = key0 + 32 > cur.len;
+        }
+        if (tail) {  // rows behind the last hold anything: neither their codes nor their scales count
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int key = 8 * r + kr;
-            const float ks = bf16_bits_to_float(sc[key]);
-            vs[r] = bf16_bits_to_float(sc[32 + key]);
+          for (int r = 0; r < 4; ++r)
+            if (key0 + 8 * r + kr >= cur.len) {
+              vs[r] = 0.f;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              float& x0 = x[r >> 1][j][2 * (r & 1)];
-              float& x1 = x[r >> 1][j][2 * (r & 1) + 1];
-              if (NT == 1 && dup) {
-                x0 += __shfl_xor_sync(0xffffffffu, x0, 2);
-                x1 += __shfl_xor_sync(0xffffffffu, x1, 2);
-              }
-              x0 *= ks * fac[j][0];
-              x1 *= ks * fac[j][1];
+              for (int j = 0; j < NT; ++j) x[r >> 1][j][2 * (r & 1)] = x[r >> 1][j][2 * (r & 1) + 1] = -INFINITY;
+            }
+        }
+        if (a.scores) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const int n = 8 * j + 2 * tq;
+            if (n < g) {
+              float* p = a.scores + (static_cast<size_t>(bh) * a.C + key0 + kr) * a.gp + n;
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (!tail || key0 + 8 * r + kr < cur.len) {
+                  if (a.gp == 1) p[8 * r] = x[r >> 1][j][2 * (r & 1)];
+                  else *reinterpret_cast<float2*>(p + 8 * r * a.gp) =
+                           make_float2(x[r >> 1][j][2 * (r & 1)], x[r >> 1][j][2 * (r & 1) + 1]);
+                }
             }
           }
-          if (tail) {  // rows behind the last hold anything: neither their codes nor their scales count
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (key0 + 8 * r + kr >= cur.len) {
-                vs[r] = 0.f;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) x[r >> 1][j][2 * (r & 1)] = x[r >> 1][j][2 * (r & 1) + 1] = -INFINITY;
-              }
-          }
-          if (a.scores) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const int n = 8 * j + 2 * tq;
-              if (n < g) {
-                float* p = a.scores + (static_cast<size_t>(bh) * a.C + key0 + kr) * a.gp + n;
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  if (!tail || key0 + 8 * r + kr < cur.len) {
-                    if (a.gp == 1) p[8 * r] = x[r >> 1][j][2 * (r & 1)];
-                    else *reinterpret_cast<float2*>(p + 8 * r * a.gp) =
-                             make_float2(x[r >> 1][j][2 * (r & 1)], x[r >> 1][j][2 * (r & 1) + 1]);
-                  }
-              }
-            }
-          }
-          // ---- the running maximum moves only when a score passes it by more than 2^8 -------
-          bool over = false;
+        }
+        // ---- p = 2^(x - m) and u = p vs 2^(m - R); m and R move only when a p passes 2^8 or a u
+        // passes 2^12, and then both are at most 1 and 2^8 in the second turn ----------------------
+        float p[2][NT][4], u[2][NT][4];
+#pragma unroll 1
+        for (int turn = 0; turn < 2; ++turn) {
+          float top_p = 0.f, top_u = 0.f;
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              over = over || fmaxf(fmaxf(x[0][j][c], x[0][j][c + 2]), fmaxf(x[1][j][c], x[1][j][c + 2])) > m_run[j][c] + 8.f;
-          if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              float al[2];
+              for (int r = 0; r < 4; ++r) {
+                const int e = 2 * (r & 1) + c;
+                p[r >> 1][j][e] = ex2_approx(x[r >> 1][j][e] - m_run[j][c]);
+                u[r >> 1][j][e] = p[r >> 1][j][e] * (vs[r] * kq[j][c]);
+                top_p = fmaxf(top_p, p[r >> 1][j][e]);
+                top_u = fmaxf(top_u, u[r >> 1][j][e]);
+              }
+          if (turn || !__any_sync(0xffffffffu, top_p > 256.f || top_u > 4096.f)) break;
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float mx = fmaxf(fmaxf(x[0][j][c], x[0][j][c + 2]), fmaxf(x[1][j][c], x[1][j][c + 2]));
+          for (int j = 0; j < NT; ++j) {
+            float al[2], be[2];
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float m_new = fmaxf(m_run[j][c], mx);
-                al[c] = ex2_approx(m_run[j][c] - m_new);
-                m_run[j][c] = m_new;
-                l_run[j][c] *= al[c];
+            for (int c = 0; c < 2; ++c) {
+              float mx = -INFINITY, ry = -INFINITY;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float y = x[r >> 1][j][2 * (r & 1) + c];
+                mx = fmaxf(mx, y);
+                ry = fmaxf(ry, y + __log2f(vs[r]));
               }
 #pragma unroll
-              for (int i = 0; i < L::MT; ++i) {
-                oacc[j][i][0] *= al[0];
-                oacc[j][i][1] *= al[1];
-                oacc[j][i][2] *= al[0];
-                oacc[j][i][3] *= al[1];
+              for (int off = 4; off < 32; off <<= 1) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                ry = fmaxf(ry, __shfl_xor_sync(0xffffffffu, ry, off));
               }
+              const float m_new = fmaxf(m_run[j][c], mx);
+              // 2^(m - R) stays a normal number
+              const float r_new = fminf(fmaxf(fmaxf(r_run[j][c], ry), m_new - 100.f), m_new + 125.f);
+              al[c] = ex2_approx(m_run[j][c] - m_new);
+              be[c] = ex2_approx(r_run[j][c] - r_new);
+              m_run[j][c] = m_new;
+              r_run[j][c] = r_new;
+              kq[j][c] = ex2_approx(m_new - r_new);
+              l_run[j][c] *= al[c];
+              ones[j][c] *= be[c];
+              ones[j][c + 2] *= be[c];
+            }
+#pragma unroll
+            for (int i = 0; i < L::MT; ++i) {
+              oacc[j][i][0] *= be[0];
+              oacc[j][i][1] *= be[1];
+              oacc[j][i][2] *= be[0];
+              oacc[j][i][3] *= be[1];
             }
           }
-          // ---- P (times the rows' scales) as the B operand -----------------------------------
-          uint32_t pb[2][NT][2];
+        }
+        // ---- u as the B operand -----------------------------------------------------------------
+        uint32_t pb[2][NT][2];
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const float p0 = ex2_approx(x[t][j][0] - m_run[j][0]), p1 = ex2_approx(x[t][j][1] - m_run[j][1]);
-              const float p2 = ex2_approx(x[t][j][2] - m_run[j][0]), p3 = ex2_approx(x[t][j][3] - m_run[j][1]);
-              l_run[j][0] += p0 + p2;
-              l_run[j][1] += p1 + p3;
-              pb[t][j][0] = movmatrix_trans(pack_bf16x2(p0 * vs[2 * t], p1 * vs[2 * t]));
-              pb[t][j][1] = movmatrix_trans(pack_bf16x2(p2 * vs[2 * t + 1], p3 * vs[2 * t + 1]));
-            }
-          // ---- O^T += V^T P^T ------------------------------------------------------------------
+          for (int j = 0; j < NT; ++j) {
+            l_run[j][0] += p[h][j][0] + p[h][j][2];
+            l_run[j][1] += p[h][j][1] + p[h][j][3];
+            pb[h][j][0] = movmatrix_trans(pack_f16x2(u[h][j][0], u[h][j][1]));
+            pb[h][j][1] = movmatrix_trans(pack_f16x2(u[h][j][2], u[h][j][3]));
+            mma_16816_f16(ones[j], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, pb[h][j][0], pb[h][j][1]);
+          }
+        // ---- O^T += V^T P^T -----------------------------------------------------------------------
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            constexpr int WPL = D / 64;  // words of a lane per key: octets WPL grp ..
-            uint32_t w[4][WPL];
+        for (int h = 0; h < 2; ++h) {
+          constexpr int WPL = D / 64;  // words of a lane per key: octets WPL grp ..
+          uint32_t w[4][WPL];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int key = 16 * t + 8 * (r >> 1) + ((2 * tq + (r & 1)) ^ (tq & 1));
-              const uint8_t* p = st + 32 * L::ROW + key * L::ROW + grp * 4 * WPL;
-              if constexpr (WPL == 1) {
-                w[r][0] = *reinterpret_cast<const uint32_t*>(p);
-              } else if constexpr (WPL == 2) {
-                const uint2 v = *reinterpret_cast<const uint2*>(p);
-                w[r][0] = v.x, w[r][1] = v.y;
-              } else {
-                const uint4 v = *reinterpret_cast<const uint4*>(p);
-                w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
-              }
-            }
+          for (int r = 0; r < 4; ++r) {
+            const int key = 16 * h + 8 * (r >> 1) + ((2 * tq + (r & 1)) ^ (tq & 1));
+            const uint8_t* q = st + L::OFF_V + key * L::ROW + grp * 4 * WPL;
             if constexpr (WPL == 1) {
-              // rows 0-7: element i of octet grp, rows 8-15: element i + 4
-              const uint32_t lo0 = __byte_perm(w[0][0], w[1][0], 0x5410), hi0 = __byte_perm(w[0][0], w[1][0], 0x7632);
-              const uint32_t lo1 = __byte_perm(w[2][0], w[3][0], 0x5410), hi1 = __byte_perm(w[2][0], w[3][0], 0x7632);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                  mma_16816(oacc[j][i], kv4_unpack_bf16(lo0, i), kv4_unpack_bf16(hi0, i), kv4_unpack_bf16(lo1, i),
-                            kv4_unpack_bf16(hi1, i), pb[t][j][0], pb[t][j][1]);
+              w[r][0] = *reinterpret_cast<const uint32_t*>(q);
+            } else if constexpr (WPL == 2) {
+              const uint2 v = *reinterpret_cast<const uint2*>(q);
+              w[r][0] = v.x, w[r][1] = v.y;
             } else {
-              // rows 0-7: element i of octet 2 s, rows 8-15: of octet 2 s + 1 (of the lane's WPL octets)
-#pragma unroll
-              for (int s = 0; s < WPL / 2; ++s)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  const uint32_t sel = half ? 0x7632 : 0x5410;
-                  const uint32_t a0 = __byte_perm(w[0][2 * s], w[1][2 * s], sel);
-                  const uint32_t a1 = __byte_perm(w[0][2 * s + 1], w[1][2 * s + 1], sel);
-                  const uint32_t a2 = __byte_perm(w[2][2 * s], w[3][2 * s], sel);
-                  const uint32_t a3 = __byte_perm(w[2][2 * s + 1], w[3][2 * s + 1], sel);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const uint32_t f0 = kv4_unpack_bf16(a0, i), f1 = kv4_unpack_bf16(a1, i);
-                    const uint32_t f2 = kv4_unpack_bf16(a2, i), f3 = kv4_unpack_bf16(a3, i);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                      mma_16816(oacc[j][s * 8 + half * 4 + i], f0, f1, f2, f3, pb[t][j][0], pb[t][j][1]);
-                  }
-                }
+              const uint4 v = *reinterpret_cast<const uint4*>(q);
+              w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
             }
           }
-          __syncwarp();  // every lane has read the stage
-          load_next();
+          // element i of a half word of t: bits 0-3 (i even) or 4-7 (i odd) of t or of t >> 8
+          auto code = [](uint32_t v, int i) { return (i & 2 ? v >> 8 : v) & (i & 1 ? 0x00f000f0u : 0x000f000fu); };
+          if constexpr (WPL == 1) {
+            // rows 0-7: element i of octet grp, rows 8-15: element i + 4
+            const uint32_t lo0 = __byte_perm(w[0][0], w[1][0], 0x5410), hi0 = __byte_perm(w[0][0], w[1][0], 0x7632);
+            const uint32_t lo1 = __byte_perm(w[2][0], w[3][0], 0x5410), hi1 = __byte_perm(w[2][0], w[3][0], 0x7632);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+                mma_16816_f16(oacc[j][i], code(lo0, i), code(hi0, i), code(lo1, i), code(hi1, i), pb[h][j][0], pb[h][j][1]);
+          } else {
+            // rows 0-7: element i of octet 2 o, rows 8-15: of octet 2 o + 1 (of the lane's WPL octets)
+#pragma unroll
+            for (int o = 0; o < WPL / 2; ++o)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const uint32_t sel = half ? 0x7632 : 0x5410;
+                const uint32_t a0 = __byte_perm(w[0][2 * o], w[1][2 * o], sel);
+                const uint32_t a1 = __byte_perm(w[0][2 * o + 1], w[1][2 * o + 1], sel);
+                const uint32_t a2 = __byte_perm(w[2][2 * o], w[3][2 * o], sel);
+                const uint32_t a3 = __byte_perm(w[2][2 * o + 1], w[3][2 * o + 1], sel);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                  for (int j = 0; j < NT; ++j)
+                    mma_16816_f16(oacc[j][o * 8 + half * 4 + i], code(a0, i), code(a1, i), code(a2, i), code(a3, i),
+                                  pb[h][j][0], pb[h][j][1]);
+              }
+          }
         }
       }
-      step(cur, left);
-    } while (left > 0 && cur.bh == bh);
+      __syncwarp();  // every lane has read the stage
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
     // ================= merge the warps ====================================================
-    float mx[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -694,61 +723,62 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
         float l = l_run[j][c];
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        l_run[j][c] = l;
-        if (grp == 0) wm[warp * NQ + 8 * j + 2 * tq + c] = m_run[j][c];
+        const int n = 8 * j + 2 * tq + c;
+        if (grp == 0) {
+          wm[warp * NQ + n] = m_run[j][c];
+          wl[warp * NQ + n] = l;
+          wr[warp * NQ + n] = r_run[j][c];
+        }
       }
-    __syncthreads();
+    named_bar_sync(1, WORKERS);
     const size_t slot = static_cast<size_t>(blockIdx.x) + bh;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int n = 8 * j + 2 * tq + c;
-        float M = kKv4Lowest;
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * NQ + n]);
-        mx[j][c] = M;
-        const float f = ex2_approx(m_run[j][c] - M);
-        if (grp == 0) wl[warp * NQ + n] = l_run[j][c] * f;
+        float R = kKv4Lowest;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) R = fmaxf(R, wr[w * NQ + n]);
+        const float f = ex2_approx(r_run[j][c] - R) * kTwo24;  // and off the codes' 2^-24
+        const float eight = ones[j][c] * f;
 #pragma unroll
         for (int i = 0; i < L::MT; ++i) {
-          oacc[j][i][c] *= f;
-          oacc[j][i][c + 2] *= f;
+          const float fi = (i & 1) ? f * 0.0625f : f;
+          oacc[j][i][c] = fmaf(oacc[j][i][c], fi, -eight);
+          oacc[j][i][c + 2] = fmaf(oacc[j][i][c + 2], fi, -eight);
         }
       }
-    __syncthreads();
-    if (warp == 0 && grp == 0) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int n = 8 * j + 2 * tq + c;
-          float l = 0.f;
-          for (int w = 0; w < NW; ++w) l += wl[w * NQ + n];
-          a.part_ml[(slot * NQ + n) * 2] = mx[j][c];
-          a.part_ml[(slot * NQ + n) * 2 + 1] = l;
-        }
-    }
-    float4* const red = reinterpret_cast<float4*>(smem + L::OFF_RED);  // [NW][NT][32]
-#pragma unroll
-    for (int i = 0; i < L::MT; ++i) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        red[(warp * NT + j) * 32 + lane] = make_float4(oacc[j][i][0], oacc[j][i][1], oacc[j][i][2], oacc[j][i][3]);
-      __syncthreads();
-      if (tid < NT * 32) {
-        float4 s = red[tid];
-        for (int w = 1; w < NW; ++w) {
-          const float4 v = red[w * NT * 32 + tid];
-          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
-        reinterpret_cast<float4*>(a.part_o)[(slot * L::MT + i) * NT * 32 + tid] = s;
+    if (tid < NQ) {
+      float M = kKv4Lowest, R = kKv4Lowest, l = 0.f;
+      for (int w = 0; w < NW; ++w) {
+        M = fmaxf(M, wm[w * NQ + tid]);
+        R = fmaxf(R, wr[w * NQ + tid]);
       }
-      __syncthreads();
+      for (int w = 0; w < NW; ++w) l += wl[w * NQ + tid] * ex2_approx(wm[w * NQ + tid] - M);
+      reinterpret_cast<float4*>(a.part_ml)[slot * NQ + tid] = make_float4(M, l, R, 0.f);
     }
+    float* const red = reinterpret_cast<float*>(smem + L::OFF_RED);  // [NW][MC][NT][32] float4
+    constexpr int RED = L::MC * NT * 128;
+#pragma unroll
+    for (int i = 0; i < L::MT; i += L::MC) {
+#pragma unroll
+      for (int c = 0; c < L::MC; ++c)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          reinterpret_cast<float4*>(red)[((warp * L::MC + c) * NT + j) * 32 + lane] =
+              make_float4(oacc[j][i + c][0], oacc[j][i + c][1], oacc[j][i + c][2], oacc[j][i + c][3]);
+      named_bar_sync(1, WORKERS);
+      for (int e = tid; e < RED; e += WORKERS) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) v += red[w * RED + e];
+        a.part_o[(slot * L::MT + i) * NT * 128 + e] = v;
+      }
+      named_bar_sync(1, WORKERS);
+    }
+    if (left > 0) next_head();
   }
-  // every copy has landed before the block ends
-  if (lane == 0)
-    for (; got < put; ++got) mbar_wait_drain(&bars[got % ST], (got / ST) & 1, 100000000ull);
 }
 
 // Joins the parts of a head by their maxima: O, LSE, and each key's weight summed over the
@@ -769,12 +799,14 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
     i0 = static_cast<int>(((b0 + 1) * n_cta - 1) / total);
     i1 = static_cast<int>((b1 * n_cta - 1) / total);
   }
+  const float4* const ml = reinterpret_cast<const float4*>(a.part_ml);
   if (tid < NQ) {
     float M = kKv4Lowest, L = 0.f;
-    for (int i = i0; i <= i1; ++i) M = fmaxf(M, a.part_ml[((static_cast<size_t>(i) + bh) * NQ + tid) * 2]);
     for (int i = i0; i <= i1; ++i) {
-      const float* ml = a.part_ml + ((static_cast<size_t>(i) + bh) * NQ + tid) * 2;
-      L += ml[1] * ex2_approx(ml[0] - M);
+      const float4 p = ml[(static_cast<size_t>(i) + bh) * NQ + tid];
+      const float m_new = fmaxf(M, p.x);
+      L = L * ex2_approx(M - m_new) + p.y * ex2_approx(p.x - m_new);
+      M = m_new;
     }
     lse2[tid] = len > 0 ? M + log2f(L) : -INFINITY;
     if (blockIdx.x == 0 && tid < g) a.lse[static_cast<size_t>(bh) * g + tid] = lse2[tid] * 0.69314718055994530942f;
@@ -788,8 +820,8 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int p = i0; p <= i1; ++p) {
         const size_t slot = static_cast<size_t>(p) + bh;
-        const float w0 = ex2_approx(a.part_ml[(slot * NQ + n) * 2] - lse2[n]);
-        const float w1 = ex2_approx(a.part_ml[(slot * NQ + n + 1) * 2] - lse2[n + 1]);
+        const float w0 = ex2_approx(ml[slot * NQ + n].z - lse2[n]);
+        const float w1 = ex2_approx(ml[slot * NQ + n + 1].z - lse2[n + 1]);
         const float4 v = reinterpret_cast<const float4*>(a.part_o)[slot * MT * NT * 32 + f];
         s.x = fmaf(v.x, w0, s.x);
         s.y = fmaf(v.y, w1, s.y);
@@ -809,12 +841,34 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
       }
     }
   if (a.acc) {
-    const int gp = a.gp;
-    for (int key = blockIdx.x * chunk + tid; key < min(len, (blockIdx.x + 1) * chunk); key += 256) {
+    // four keys of a thread at a time, so that their loads are under way together
+    const int gp = a.gp, end = min(len, (blockIdx.x + 1) * chunk);
+    for (int key = blockIdx.x * chunk + tid; key < end; key += 1024) {
+      float w[4], old[4];
       const size_t row = static_cast<size_t>(bh) * a.C + key;
-      float w = 0.f;
-      for (int h = 0; h < g; ++h) w += ex2_approx(a.scores[row * gp + h] - lse2[h]);
-      a.acc[row] += w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = 0.f;
+        old[i] = key + 256 * i < end ? a.acc[row + 256 * i] : 0.f;
+      }
+      if (gp == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (key + 256 * i < end) w[i] = ex2_approx(a.scores[row + 256 * i] - lse2[0]);
+      } else {
+        for (int h = 0; h < g; h += 2) {
+          const float l0 = lse2[h], l1 = h + 1 < g ? lse2[h + 1] : INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key + 256 * i < end) {
+              const float2 v = *reinterpret_cast<const float2*>(a.scores + (row + 256 * i) * gp + h);
+              w[i] += ex2_approx(v.x - l0) + (h + 1 < g ? ex2_approx(v.y - l1) : 0.f);
+            }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (key + 256 * i < end) a.acc[row + 256 * i] = old[i] + w[i];
     }
   }
 }
