@@ -46,6 +46,23 @@ Kv4Plan kv4_plan(int B, int H, int Hkv, int C, int d, bool weights) {
   return p;
 }
 
+// A kernel that is launched while the one before it on the stream still runs, and waits for it
+// on the device (griddepcontrol.wait).
+template <typename... Params, typename... Args>
+int launch_after(void (*kern)(Params...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
 template <int D, int NT>
 int launch_kv4_decode(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
   using L = fa::Kv4Cfg<D, NT>;
@@ -55,19 +72,49 @@ int launch_kv4_decode(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
   kern<<<a.grid, L::THREADS, L::BYTES, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
-  // the second kernel is launched while the first one runs and waits for it on the device
   const int chunk = 1024;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.acc ? (a.C + chunk - 1) / chunk : 1, a.BHkv);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fa::fa_kv4_combine_kernel<D, NT>, a, chunk);
-  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+  return launch_after(fa::fa_kv4_combine_kernel<D, NT>, dim3(a.acc ? (a.C + chunk - 1) / chunk : 1, a.BHkv), dim3(256), s,
+                      a, chunk);
+}
+
+// The key weights' plan: query rows per step (64 where the window is no longer, and at d = 256,
+// where a 128-row tile would leave the ring one place), CTAs, and the workspace's parts in bytes.
+struct KeyWeightsPlan {
+  int qt, ranges, grid;
+  size_t part, first, bytes;
+};
+
+KeyWeightsPlan key_weights_plan(int B, int H, int Hkv, int N, int d, int window) {
+  KeyWeightsPlan p;
+  p.qt = d == 256 || window <= 64 ? 64 : 128;
+  p.ranges = (N + 255) / 256;
+  const long long items = static_cast<long long>(B) * Hkv * p.ranges;
+  const long long steps = items * (H / Hkv) * ((std::min(window, N) + p.qt - 1) / p.qt + 1);
+  p.grid = static_cast<int>(std::min<long long>(148, steps));
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  p.part = 0;
+  p.first = up((static_cast<size_t>(p.grid) + items) * 256 * 4);
+  p.bytes = p.first + up((static_cast<size_t>(B) * p.ranges + 1) * 8);
+  return p;
+}
+
+template <int D, int QT>
+int launch_key_weights(const void* q, const void* k, int B, int H, int Hkv, int N, const fa::KeyWeightsArgs& a,
+                       cudaStream_t s) {
+  using C = fa::KeyWeightsCfg<D, QT>;
+  CUtensorMap mq, mk;
+  int st;
+  const auto dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if ((st = encode_qkv_map(&mq, q, dt, 2, D, N, B * H, CU_TENSOR_MAP_SWIZZLE_128B, QT)) != FA_OK) return st;
+  if ((st = encode_qkv_map(&mk, k, dt, 2, D, N, B * Hkv)) != FA_OK) return st;
+  auto kern = fa::fa_key_weights_kernel<D, QT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return cuda_fail(e);
+  kern<<<a.grid, 384, C::SMEM_BYTES, s>>>(mq, mk, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  return launch_after(fa::fa_key_weights_sum_kernel<QT>, dim3(static_cast<unsigned>(static_cast<long long>(B) * Hkv * a.ranges)),
+                      dim3(256), s, a);
 }
 
 }  // namespace
@@ -76,7 +123,8 @@ extern "C" {
 
 size_t fa_key_weights_workspace_bytes(int B, int H, int H_kv, int N, int d, int window) {
   if (B < 1 || H < 1 || H_kv < 1 || N < 1 || window < 1 || H % H_kv != 0 || !head_dim_ok(d)) return 0;
-  return 256;
+  if (!sizes_fit(B, H, N, d)) return 0;
+  return key_weights_plan(B, H, H_kv, N, d, window).bytes;
 }
 
 int fa_key_weights(const void* q, const void* k, const float* lse, float* w, const int* n_rows, int B, int H, int H_kv,
@@ -90,12 +138,16 @@ int fa_key_weights(const void* q, const void* k, const float* lse, float* w, con
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return FA_ERR_ALIGNMENT;
   if (workspace_bytes < fa_key_weights_workspace_bytes(B, H, H_kv, N, d, window)) return FA_ERR_INVALID_ARG;
+  const KeyWeightsPlan p = key_weights_plan(B, H, H_kv, N, d, window);
+  if (static_cast<long long>(B) * H_kv * p.ranges >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   fa::KeyWeightsArgs a;
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.k = static_cast<const __nv_bfloat16*>(k);
   a.lse = lse;
   a.w = w;
   a.n_rows = n_rows;
+  a.part = reinterpret_cast<float*>(ws + p.part);
+  a.first = reinterpret_cast<long long*>(ws + p.first);
+  a.B = B;
   a.N = N;
   a.ldw = ldw;
   a.H = H;
@@ -103,14 +155,16 @@ int fa_key_weights(const void* q, const void* k, const float* lse, float* w, con
   a.g = H / H_kv;
   a.window = std::min(window, N);
   a.causal = causal ? 1 : 0;
-  a.ktiles = (N + 127) / 128;
+  a.ranges = p.ranges;
+  a.grid = p.grid;
   a.scale_log2 = scale * 1.4426950408889634f;
-  const unsigned grid = static_cast<unsigned>(static_cast<long long>(B) * H_kv * a.ktiles);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 64) fa::fa_key_weights_kernel<64><<<grid, 128, 0, s>>>(a);
-  else if (d == 128) fa::fa_key_weights_kernel<128><<<grid, 128, 0, s>>>(a);
-  else fa::fa_key_weights_kernel<256><<<grid, 128, 0, s>>>(a);
-  return launched();
+  if (d == 256) return launch_key_weights<256, 64>(q, k, B, H, H_kv, N, a, s);
+  if (d == 64)
+    return p.qt == 64 ? launch_key_weights<64, 64>(q, k, B, H, H_kv, N, a, s)
+                      : launch_key_weights<64, 128>(q, k, B, H, H_kv, N, a, s);
+  return p.qt == 64 ? launch_key_weights<128, 64>(q, k, B, H, H_kv, N, a, s)
+                    : launch_key_weights<128, 128>(q, k, B, H, H_kv, N, a, s);
 }
 
 int fa_evict_keep(const float* w, const int* lens, int* idx, int* count, int B, int H_kv, int C, int keep, int n_recent,
