@@ -77,43 +77,41 @@ int launch_kv4_decode(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
                       a, chunk);
 }
 
-// The key weights' plan: query rows per step (64 where the window is no longer, and at d = 256,
-// where a 128-row tile would leave the ring one place), CTAs, and the workspace's parts in bytes.
+// The key weights' plan: CTAs, and the workspace's parts in bytes.
 struct KeyWeightsPlan {
-  int qt, ranges, grid;
+  int ranges, grid;
   size_t part, first, bytes;
 };
 
-KeyWeightsPlan key_weights_plan(int B, int H, int Hkv, int N, int d, int window) {
+KeyWeightsPlan key_weights_plan(int B, int H, int Hkv, int N, int window) {
   KeyWeightsPlan p;
-  p.qt = d == 256 || window <= 64 ? 64 : 128;
   p.ranges = (N + 255) / 256;
   const long long items = static_cast<long long>(B) * Hkv * p.ranges;
-  const long long steps = items * (H / Hkv) * ((std::min(window, N) + p.qt - 1) / p.qt + 1);
-  p.grid = static_cast<int>(std::min<long long>(148, steps));
+  const long long subs = (std::min(window, N) + 63ll) / 64 * (H / Hkv);
+  p.grid = static_cast<int>(std::min<long long>(148, items * ((subs + 1) / 2)));
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   p.part = 0;
-  p.first = up((static_cast<size_t>(p.grid) + items) * 256 * 4);
+  p.first = up((static_cast<size_t>(p.grid) + items) * 512 * 4);
   p.bytes = p.first + up((static_cast<size_t>(B) * p.ranges + 1) * 8);
   return p;
 }
 
-template <int D, int QT>
+template <int D>
 int launch_key_weights(const void* q, const void* k, int B, int H, int Hkv, int N, const fa::KeyWeightsArgs& a,
                        cudaStream_t s) {
-  using C = fa::KeyWeightsCfg<D, QT>;
+  using C = fa::KeyWeightsCfg<D>;
   CUtensorMap mq, mk;
   int st;
   const auto dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if ((st = encode_qkv_map(&mq, q, dt, 2, D, N, B * H, CU_TENSOR_MAP_SWIZZLE_128B, QT)) != FA_OK) return st;
+  if ((st = encode_qkv_map(&mq, q, dt, 2, D, N, B * H, CU_TENSOR_MAP_SWIZZLE_128B, 64)) != FA_OK) return st;
   if ((st = encode_qkv_map(&mk, k, dt, 2, D, N, B * Hkv)) != FA_OK) return st;
-  auto kern = fa::fa_key_weights_kernel<D, QT>;
+  auto kern = fa::fa_key_weights_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
-  kern<<<a.grid, 384, C::SMEM_BYTES, s>>>(mq, mk, a);
+  kern<<<a.grid, fa::kKeyWeightsThreads, C::SMEM_BYTES, s>>>(mq, mk, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
-  return launch_after(fa::fa_key_weights_sum_kernel<QT>, dim3(static_cast<unsigned>(static_cast<long long>(B) * Hkv * a.ranges)),
+  return launch_after(fa::fa_key_weights_sum_kernel, dim3(static_cast<unsigned>(static_cast<long long>(B) * Hkv * a.ranges)),
                       dim3(256), s, a);
 }
 
@@ -124,7 +122,7 @@ extern "C" {
 size_t fa_key_weights_workspace_bytes(int B, int H, int H_kv, int N, int d, int window) {
   if (B < 1 || H < 1 || H_kv < 1 || N < 1 || window < 1 || H % H_kv != 0 || !head_dim_ok(d)) return 0;
   if (!sizes_fit(B, H, N, d)) return 0;
-  return key_weights_plan(B, H, H_kv, N, d, window).bytes;
+  return key_weights_plan(B, H, H_kv, N, window).bytes;
 }
 
 int fa_key_weights(const void* q, const void* k, const float* lse, float* w, const int* n_rows, int B, int H, int H_kv,
@@ -138,7 +136,7 @@ int fa_key_weights(const void* q, const void* k, const float* lse, float* w, con
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return FA_ERR_ALIGNMENT;
   if (workspace_bytes < fa_key_weights_workspace_bytes(B, H, H_kv, N, d, window)) return FA_ERR_INVALID_ARG;
-  const KeyWeightsPlan p = key_weights_plan(B, H, H_kv, N, d, window);
+  const KeyWeightsPlan p = key_weights_plan(B, H, H_kv, N, window);
   if (static_cast<long long>(B) * H_kv * p.ranges >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   fa::KeyWeightsArgs a;
@@ -158,13 +156,11 @@ int fa_key_weights(const void* q, const void* k, const float* lse, float* w, con
   a.ranges = p.ranges;
   a.grid = p.grid;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.neg_inv_scale = -1.f / scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 256) return launch_key_weights<256, 64>(q, k, B, H, H_kv, N, a, s);
-  if (d == 64)
-    return p.qt == 64 ? launch_key_weights<64, 64>(q, k, B, H, H_kv, N, a, s)
-                      : launch_key_weights<64, 128>(q, k, B, H, H_kv, N, a, s);
-  return p.qt == 64 ? launch_key_weights<128, 64>(q, k, B, H, H_kv, N, a, s)
-                    : launch_key_weights<128, 128>(q, k, B, H, H_kv, N, a, s);
+  if (d == 64) return launch_key_weights<64>(q, k, B, H, H_kv, N, a, s);
+  if (d == 128) return launch_key_weights<128>(q, k, B, H, H_kv, N, a, s);
+  return launch_key_weights<256>(q, k, B, H, H_kv, N, a, s);
 }
 
 int fa_evict_keep(const float* w, const int* lens, int* idx, int* count, int B, int H_kv, int C, int keep, int n_recent,

@@ -289,7 +289,8 @@ template <int D, int NT>
 __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kernel(const Kv4DecodeArgs a) {
   using L = Kv4Cfg<D, NT>;
   constexpr int NW = L::NW, ST = L::STAGES, NQ = 8 * NT, WORKERS = NW * 32;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grp = lane >> 2, tq = lane & 3;
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
