@@ -115,6 +115,36 @@ int launch_key_weights(const void* q, const void* k, int B, int H, int Hkv, int 
                       dim3(256), s, a);
 }
 
+// Eviction: CTAs per head (a cluster of up to sixteen), while the grid stays within the SMs.
+template <bool SLOTS, int ITEMS>
+cudaError_t launch_evict_items(const cudaLaunchConfig_t& cfg, const fa::EvictArgs& a) {
+  const cudaError_t e = cudaFuncSetAttribute(fa::fa_evict_kernel<SLOTS, ITEMS>,
+                                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, fa::fa_evict_kernel<SLOTS, ITEMS>, a) : e;
+}
+
+template <bool SLOTS>
+int launch_evict(fa::EvictArgs a, int heads, int rows, cudaStream_t s) {
+  int S = 1;
+  while (S < fa::kEvictMaxCluster && rows > 4096 * S && 2ll * S * heads <= 148) S *= 2;
+  a.ctas = S;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(heads) * S);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int per = (rows + S - 1) / S;
+  const cudaError_t e = per <= 4096   ? launch_evict_items<SLOTS, 4>(cfg, a)
+                        : per <= 8192 ? launch_evict_items<SLOTS, 8>(cfg, a)
+                                      : launch_evict_items<SLOTS, 16>(cfg, a);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -168,7 +198,7 @@ int fa_evict_keep(const float* w, const int* lens, int* idx, int* count, int B, 
   if (!w || !idx || !count) return FA_ERR_INVALID_ARG;
   if (B < 1 || H_kv < 1 || C < 1 || keep < 1 || n_recent < 0 || n_sink < 0) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(n_recent) + n_sink > keep) return FA_ERR_INVALID_ARG;
-  if (C > (1 << 30) || keep > (1 << 30) || static_cast<long long>(B) * H_kv >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (C > (1 << 30) || keep > (1 << 30) || static_cast<long long>(B) * H_kv >= (1ll << 30)) return FA_ERR_UNSUPPORTED;
   if (!aligned4(w) || !aligned4(lens) || !aligned4(idx) || !aligned4(count)) return FA_ERR_ALIGNMENT;
   fa::EvictArgs a = {};
   a.w = w;
@@ -180,8 +210,7 @@ int fa_evict_keep(const float* w, const int* lens, int* idx, int* count, int B, 
   a.n_out = keep;
   a.n_recent = n_recent;
   a.n_sink = n_sink;
-  fa::fa_evict_kernel<false><<<B * H_kv, fa::kEvictThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launched();
+  return launch_evict<false>(a, B * H_kv, C, static_cast<cudaStream_t>(stream));
 }
 
 int fa_evict_slots(const float* acc, const int* pos, int* lens, const int* seen, int* slots, int B, int H_kv, int C,
@@ -189,7 +218,7 @@ int fa_evict_slots(const float* acc, const int* pos, int* lens, const int* seen,
   if (!acc || !pos || !lens || !seen || !slots) return FA_ERR_INVALID_ARG;
   if (B < 1 || H_kv < 1 || C < 1 || T < 1 || n_recent < 0 || n_sink < 0) return FA_ERR_INVALID_ARG;
   if (budget < 1 || budget > C || T > budget) return FA_ERR_INVALID_ARG;
-  if (C > (1 << 30) || static_cast<long long>(B) * H_kv >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (C > (1 << 30) || static_cast<long long>(B) * H_kv >= (1ll << 30)) return FA_ERR_UNSUPPORTED;
   if (!aligned4(acc) || !aligned4(pos) || !aligned4(lens) || !aligned4(seen) || !aligned4(slots)) return FA_ERR_ALIGNMENT;
   fa::EvictArgs a = {};
   a.w = acc;
@@ -203,8 +232,7 @@ int fa_evict_slots(const float* acc, const int* pos, int* lens, const int* seen,
   a.budget = budget;
   a.n_recent = n_recent;
   a.n_sink = n_sink;
-  fa::fa_evict_kernel<true><<<B * H_kv, fa::kEvictThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launched();
+  return launch_evict<true>(a, B * H_kv, budget, static_cast<cudaStream_t>(stream));
 }
 
 int fa_kv4_append(const void* k, const void* v, const float* signs, const float* w, const int* rows, const int* slots,

@@ -27,7 +27,11 @@ def _weights(seed, *shape, kind="heavy"):
     (1, 1, 1, 1, 0, 0, "heavy"), (1, 2, 100, 30, 5, 4, "heavy"), (2, 3, 1000, 999, 0, 0, "ties"),
     (2, 2, 1025, 64, 32, 4, "ties"), (1, 2, 5000, 4097, 100, 0, "odd"), (1, 1, 70001, 20000, 50, 4, "heavy"),
     (1, 2, 3001, 1500, 0, 0, "near"), (1, 1, 300, 400, 10, 4, "heavy"), (1, 1, 40000, 1, 0, 0, "near"),
-    (2, 80, 257, 100, 3, 3, "odd")])
+    (2, 80, 257, 100, 3, 3, "odd"),
+    # many heads: one CTA each, whose rows do not fit its registers
+    (2, 80, 20001, 5000, 50, 4, "heavy"), (1, 150, 33000, 17000, 0, 0, "ties"),
+    # a cluster whose rows do not, and a list of equals that overflows
+    (1, 1, 140000, 60000, 10, 4, "heavy"), (1, 2, 60000, 30001, 10, 4, "near")])
 def test_keep(B, Hkv, C, keep, recent, sink, kind):
     from exact_io_aware_85_b200 import fa
     w = _weights(C + keep, B, Hkv, C, kind=kind)
@@ -47,7 +51,9 @@ def test_keep(B, Hkv, C, keep, recent, sink, kind):
 @pytest.mark.parametrize("B,Hkv,C,budget,T,recent,sink,kind", [
     (1, 1, 1, 1, 1, 0, 0, "heavy"), (2, 2, 128, 100, 1, 10, 4, "heavy"), (1, 3, 1000, 1000, 17, 200, 4, "ties"),
     (2, 1, 4096, 4095, 1, 256, 4, "ties"), (1, 1, 70000, 66001, 500, 1000, 4, "heavy"), (1, 2, 500, 500, 500, 10, 2, "odd"),
-    (1, 2, 2048, 2000, 64, 1999, 4, "near"), (3, 50, 300, 256, 2, 8, 2, "odd")])
+    (1, 2, 2048, 2000, 64, 1999, 4, "near"), (3, 50, 300, 256, 2, 8, 2, "odd"),
+    (1, 150, 20100, 20001, 300, 100, 4, "heavy"), (1, 150, 33000, 33000, 1, 100, 4, "ties"),
+    (1, 1, 150000, 140000, 1000, 100, 4, "near"), (1, 2, 140000, 140000, 1, 100, 4, "heavy")])
 def test_slots(B, Hkv, C, budget, T, recent, sink, kind):
     from exact_io_aware_85_b200 import fa
     acc = _weights(C + T, B, Hkv, C, kind=kind)
