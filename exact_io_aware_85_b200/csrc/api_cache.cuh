@@ -270,7 +270,8 @@ int fa_kv4_append(const void* k, const void* v, const float* signs, const float*
   a.C = C;
   a.ldw = ldw;
   a.Hkv = H_kv;
-  a.tblocks = (T + 7) / 8;
+  const int rows_per_block = 8 * (512 / d);
+  a.tblocks = (T + rows_per_block - 1) / rows_per_block;
   const long long blocks = static_cast<long long>(B) * H_kv * a.tblocks;
   if (blocks >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks), 2);
@@ -304,7 +305,8 @@ int fa_kv4_read(const void* kc, const void* ks, const void* vc, const void* vs, 
   a.T = T;
   a.C = C;
   a.first = first;
-  a.tblocks = (T + 7) / 8;
+  const int rows_per_block = 8 * (512 / d);
+  a.tblocks = (T + rows_per_block - 1) / rows_per_block;
   const long long blocks = static_cast<long long>(B) * H_kv * a.tblocks;
   if (blocks >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks), 2);

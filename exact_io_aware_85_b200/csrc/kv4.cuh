@@ -39,66 +39,141 @@ struct Kv4AppendArgs {
   int tblocks;             // blocks per (b, head)
 };
 
-// One warp per row; lane l holds elements [l E, (l + 1) E).  blockIdx.y: keys, values.
+// D / 16 lanes hold a row, 16 elements each: two chunks of 8 that lie half a row apart, so that
+// both of a lane's 16-byte loads belong to whole lines of its row's lanes.
+template <int D>
+struct Kv4Row {
+  static constexpr int LANES = D / 16, ROWS = 32 / LANES;  // lanes per row, rows per warp
+};
+
+// y <- H y over the lanes of each row (element bits 0-2 in a chunk, then the lane's, then the
+// chunk), the stages in ascending order: the same additions whatever holds the row.
+template <int D>
+__device__ __forceinline__ void kv4_hadamard(float (&y)[16], int lane) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const float p = y[i], q = y[i + 1];
+    y[i] = p + q;
+    y[i + 1] = p - q;
+  }
+  float2* const z = reinterpret_cast<float2*>(y);  // the other stages keep the pairs together
+#pragma unroll
+  for (int h = 1; h < 4; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & h)) {
+        const float2 p = z[i], q = z[i + h];
+        z[i] = fadd2(p, q);
+        z[i + h] = fsub2(p, q);
+      }
+#pragma unroll
+  for (int h = 1; h < Kv4Row<D>::LANES; h <<= 1) {
+    const float sign = (lane & h) ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      z[i] = ffma2(make_float2(sign, sign), z[i],
+                   make_float2(__shfl_xor_sync(0xffffffffu, z[i].x, h), __shfl_xor_sync(0xffffffffu, z[i].y, h)));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = z[i], q = z[i + 4];
+    z[i] = fadd2(p, q);
+    z[i + 4] = fsub2(p, q);
+  }
+}
+__device__ __forceinline__ void kv4_unpack_bf16x8(const uint4& v, float* y) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = __uint_as_float(w[i] << 16);
+    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// blockIdx.y: keys, values.  What a row costs in instructions comes close to what it costs in
+// bytes: the quotient y / s is formed with the reciprocal, and only where it comes out next to the
+// border of two codes (an exact tie, often, as s and an unrotated y have 8 bits) by a division.
 template <int D>
 __global__ void __launch_bounds__(256) fa_kv4_append_kernel(const Kv4AppendArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  using R = Kv4Row<D>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % R::LANES;
   const int bh = blockIdx.x / a.tblocks;
-  const int t = (blockIdx.x % a.tblocks) * 8 + warp;
+  const int t = (blockIdx.x % a.tblocks) * (8 * R::ROWS) + warp * R::ROWS + lane / R::LANES;
   const bool is_v = blockIdx.y == 1;
   const int n_new = a.n_new ? min(a.n_new[bh], a.T) : a.T;
-  if (t >= n_new) return;
   const long long bt = static_cast<long long>(bh) * a.T + t;
-  const int src = a.rows ? a.rows[bt] : t;
-  const long long dst = a.slots ? a.slots[bt] : (a.start ? static_cast<long long>(a.start[bh]) : 0) + t;
-  if (src < 0 || src >= a.N || dst < 0 || dst >= a.C) return;
-  const __nv_bfloat16* x = (is_v ? a.v : a.k) + (static_cast<size_t>(bh) * a.N + src) * D + lane * E;
-  float y[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) y[i] = __bfloat162float(x[i]);
+  bool live = t < n_new;
+  int src = -1;
+  long long dst = -1;
+  if (live) {
+    src = a.rows ? a.rows[bt] : t;
+    dst = a.slots ? a.slots[bt] : (a.start ? static_cast<long long>(a.start[bh]) : 0) + t;
+    live = src >= 0 && src < a.N && dst >= 0 && dst < a.C;
+  }
+  __align__(8) float y[16];
+  uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+  if (live) {
+    const uint4* x = reinterpret_cast<const uint4*>((is_v ? a.v : a.k) + (static_cast<size_t>(bh) * a.N + src) * D);
+    v0 = x[sub];
+    v1 = x[sub + R::LANES];
+  }
+  kv4_unpack_bf16x8(v0, y);
+  kv4_unpack_bf16x8(v1, y + 8);
   if (!is_v && a.signs) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) y[i] *= a.signs[lane * E + i];
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int h = 1; h < E; h <<= 1)
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (!(i & h)) {
-          const float p = y[i], q = y[i + h];
-          y[i] = p + q;
-          y[i + h] = p - q;
-        }
-#pragma unroll
-    for (int h = 1; h < 32; h <<= 1)
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float o = __shfl_xor_sync(0xffffffffu, y[i], h);
-        y[i] = (lane & h) ? o - y[i] : y[i] + o;
-      }
+      for (int i = 0; i < 8; ++i) y[8 * c + i] *= a.signs[(sub + c * R::LANES) * 8 + i];
+    kv4_hadamard<D>(y, lane);
   }
   // the largest magnitude by its bits: an infinity or a NaN in the row wins
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
-  top = __reduce_max_sync(0xffffffffu, top);
+  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
+#pragma unroll
+  for (int h = 1; h < R::LANES; h <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, h));
   const bool finite = top < 0x7f800000u;
   const __nv_bfloat16 sb = finite ? __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.f))
                                   : __ushort_as_bfloat16(static_cast<unsigned short>(0x7fff));
   const float s = __bfloat162float(sb);
-  uint32_t packed = 0;
+  // codes as the low bits of 1.5 2^23 + c + 8; |y| <= amax, so |c| <= 7 where s is a normal number
+  uint32_t packed[2] = {0u, 0u};
+  const float kMagic = 12582912.f;
+  if (finite && s >= 1e-30f) {
+    const float inv = __frcp_rn(s);
+    const float2 inv2 = make_float2(inv, inv), magic2 = make_float2(kMagic, kMagic);
+    float off = 0.f;
+    __align__(8) float u[16];
+    const float2* const z = reinterpret_cast<const float2*>(y);
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    float c = 0.f;
-    if (finite && s > 0.f) c = fminf(7.f, fmaxf(-7.f, rintf(__fdiv_rn(y[i], s))));
-    packed |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * i);
+    for (int i = 0; i < 8; ++i) {
+      const float2 q = fmul2(z[i], inv2), m = fadd2(q, magic2), r = fsub2(q, fsub2(m, magic2));
+      u[2 * i] = m.x, u[2 * i + 1] = m.y;
+      off = fmax3(off, fabsf(r.x), fabsf(r.y));
+    }
+    if (off > 0.4999f) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float q = y[i] * inv;
+        if (fabsf(q - (u[i] - kMagic)) > 0.4999f) u[i] = rintf(__fdiv_rn(y[i], s)) + kMagic;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) packed[i >> 3] |= ((__float_as_uint(u[i]) + 8u) & 15u) << (4 * (i & 7));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float c = 0.f;
+      if (finite && s > 0.f) c = fminf(7.f, fmaxf(-7.f, rintf(__fdiv_rn(y[i], s))));
+      packed[i >> 3] |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * (i & 7));
+    }
   }
+  if (!live) return;
   const size_t row = static_cast<size_t>(bh) * a.C + dst;
-  uint8_t* codes = (is_v ? a.vc : a.kc) + row * (D / 2) + lane * (E / 2);
-  if constexpr (E == 2) *codes = static_cast<uint8_t>(packed);
-  else if constexpr (E == 4) *reinterpret_cast<uint16_t*>(codes) = static_cast<uint16_t>(packed);
-  else *reinterpret_cast<uint32_t*>(codes) = packed;
-  if (lane == 0) {
+  uint32_t* codes = reinterpret_cast<uint32_t*>((is_v ? a.vc : a.kc) + row * (D / 2));
+  codes[sub] = packed[0];
+  codes[sub + R::LANES] = packed[1];
+  if (sub == 0) {
     (is_v ? a.vs : a.ks)[row] = sb;
     if (!is_v) {
       if (a.acc) a.acc[row] = a.w ? a.w[static_cast<size_t>(bh) * a.ldw + src] : 0.f;
@@ -128,51 +203,45 @@ struct Kv4ReadArgs {
 // exact in fp32): x = signs (s / d) H c, rounded once, to bf16.
 template <int D>
 __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const Kv4ReadArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  using R = Kv4Row<D>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % R::LANES;
   const int bh = blockIdx.x / a.tblocks;
-  const int t = (blockIdx.x % a.tblocks) * 8 + warp;
+  const int t = (blockIdx.x % a.tblocks) * (8 * R::ROWS) + warp * R::ROWS + lane / R::LANES;
   const bool is_v = blockIdx.y == 1;
-  if (t >= a.T) return;
   const long long bt = static_cast<long long>(bh) * a.T + t;
-  const long long r = a.slots ? a.slots[bt] : static_cast<long long>(a.first) + t;
   const int len = a.lens ? min(a.lens[bh], a.C) : a.C;
-  float y[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) y[i] = 0.f;
-  if (r >= 0 && r < len) {
+  long long r = -1;
+  if (t < a.T) r = a.slots ? a.slots[bt] : static_cast<long long>(a.first) + t;
+  const bool live = r >= 0 && r < len;
+  uint32_t w[2] = {0x88888888u, 0x88888888u};  // zeros
+  float s = 0.f;
+  if (live) {
     const size_t row = static_cast<size_t>(bh) * a.C + r;
-    const uint8_t* codes = (is_v ? a.vc : a.kc) + row * (D / 2) + lane * (E / 2);
-#pragma unroll
-    for (int i = 0; i < E; ++i) y[i] = static_cast<float>(static_cast<int>((codes[i / 2] >> (4 * (i & 1))) & 15) - 8);
-    float s = __bfloat162float((is_v ? a.vs : a.ks)[row]);
-    if (!is_v && a.signs) {
-#pragma unroll
-      for (int h = 1; h < E; h <<= 1)
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (!(i & h)) {
-            const float p = y[i], q = y[i + h];
-            y[i] = p + q;
-            y[i + h] = p - q;
-          }
-#pragma unroll
-      for (int h = 1; h < 32; h <<= 1)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float o = __shfl_xor_sync(0xffffffffu, y[i], h);
-          y[i] = (lane & h) ? o - y[i] : y[i] + o;
-        }
-      s *= 1.f / D;
-#pragma unroll
-      for (int i = 0; i < E; ++i) y[i] *= a.signs[lane * E + i];
-    }
-#pragma unroll
-    for (int i = 0; i < E; ++i) y[i] *= s;
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>((is_v ? a.vc : a.kc) + row * (D / 2));
+    w[0] = codes[sub];
+    w[1] = codes[sub + R::LANES];
+    s = __bfloat162float((is_v ? a.vs : a.ks)[row]);
   }
-  __nv_bfloat16* out = (is_v ? a.v : a.k) + bt * D + lane * E;
+  __align__(8) float y[16];
 #pragma unroll
-  for (int i = 0; i < E; ++i) out[i] = __float2bfloat16_rn(y[i]);
+  for (int i = 0; i < 16; ++i)  // 2^23 + code, less 2^23 + 8
+    y[i] = __uint_as_float(0x4B000000u | ((w[i >> 3] >> (4 * (i & 7))) & 15u)) - 8388616.f;
+  if (!is_v && a.signs) {
+    kv4_hadamard<D>(y, lane);
+    s *= 1.f / D;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[8 * c + i] *= a.signs[(sub + c * R::LANES) * 8 + i];
+  }
+  if (t >= a.T) return;
+  uint4* out = reinterpret_cast<uint4*>((is_v ? a.v : a.k) + bt * D);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const float* z = y + 8 * c;
+    out[sub + c * R::LANES] = make_uint4(pack_bf16x2(z[0] * s, z[1] * s), pack_bf16x2(z[2] * s, z[3] * s),
+                                         pack_bf16x2(z[4] * s, z[5] * s), pack_bf16x2(z[6] * s, z[7] * s));
+  }
 }
 
 // ---------------------------------------------------------------------------
