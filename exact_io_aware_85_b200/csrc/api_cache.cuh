@@ -5,6 +5,9 @@
 
 namespace {
 
+// rows of k and v enter and leave the cache by 32-byte accesses
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
 // Sizes of a cache: C rows per (b, key/value head), a multiple of 128 and at most 2^30.
@@ -243,7 +246,7 @@ int fa_kv4_append(const void* k, const void* v, const float* signs, const float*
   int st = check_cache(B, H_kv, C, d);
   if (st != FA_OK) return st;
   if (!sizes_fit(B, H_kv, N, d) || !sizes_fit(B, H_kv, T, d)) return FA_ERR_UNSUPPORTED;
-  if (!aligned16(k) || !aligned16(v) || !aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs) ||
+  if (!aligned32(k) || !aligned32(v) || !aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs) ||
       !aligned16(acc) || !aligned16(pos))
     return FA_ERR_ALIGNMENT;
   if (!aligned4(signs) || !aligned4(w) || !aligned4(rows) || !aligned4(slots) || !aligned4(start) || !aligned4(n_new) ||
@@ -270,15 +273,15 @@ int fa_kv4_append(const void* k, const void* v, const float* signs, const float*
   a.C = C;
   a.ldw = ldw;
   a.Hkv = H_kv;
-  const int rows_per_block = 8 * (512 / d);
+  const int rows_per_block = 32;
   a.tblocks = (T + rows_per_block - 1) / rows_per_block;
   const long long blocks = static_cast<long long>(B) * H_kv * a.tblocks;
   if (blocks >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 64) fa::fa_kv4_append_kernel<64><<<grid, 256, 0, s>>>(a);
-  else if (d == 128) fa::fa_kv4_append_kernel<128><<<grid, 256, 0, s>>>(a);
-  else fa::fa_kv4_append_kernel<256><<<grid, 256, 0, s>>>(a);
+  if (d == 64) fa::fa_kv4_append_kernel<64><<<grid, 128, 0, s>>>(a);
+  else if (d == 128) fa::fa_kv4_append_kernel<128><<<grid, 128, 0, s>>>(a);
+  else fa::fa_kv4_append_kernel<256><<<grid, 128, 0, s>>>(a);
   return launched();
 }
 
@@ -289,7 +292,7 @@ int fa_kv4_read(const void* kc, const void* ks, const void* vc, const void* vs, 
   int st = check_cache(B, H_kv, C, d);
   if (st != FA_OK) return st;
   if (!sizes_fit(B, H_kv, T, d)) return FA_ERR_UNSUPPORTED;
-  if (!aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs) || !aligned16(k) || !aligned16(v))
+  if (!aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs) || !aligned32(k) || !aligned32(v))
     return FA_ERR_ALIGNMENT;
   if (!aligned4(signs) || !aligned4(slots) || !aligned4(lens)) return FA_ERR_ALIGNMENT;
   fa::Kv4ReadArgs a;
@@ -305,15 +308,15 @@ int fa_kv4_read(const void* kc, const void* ks, const void* vc, const void* vs, 
   a.T = T;
   a.C = C;
   a.first = first;
-  const int rows_per_block = 8 * (512 / d);
+  const int rows_per_block = 32;
   a.tblocks = (T + rows_per_block - 1) / rows_per_block;
   const long long blocks = static_cast<long long>(B) * H_kv * a.tblocks;
   if (blocks >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 64) fa::fa_kv4_read_kernel<64><<<grid, 256, 0, s>>>(a);
-  else if (d == 128) fa::fa_kv4_read_kernel<128><<<grid, 256, 0, s>>>(a);
-  else fa::fa_kv4_read_kernel<256><<<grid, 256, 0, s>>>(a);
+  if (d == 64) fa::fa_kv4_read_kernel<64><<<grid, 128, 0, s>>>(a);
+  else if (d == 128) fa::fa_kv4_read_kernel<128><<<grid, 128, 0, s>>>(a);
+  else fa::fa_kv4_read_kernel<256><<<grid, 128, 0, s>>>(a);
   return launched();
 }
 

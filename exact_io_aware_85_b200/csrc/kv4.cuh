@@ -16,6 +16,15 @@ namespace fa {
 
 constexpr int kKv4Rows = 128;  // cache capacities are multiples of this many rows
 
+// D (16x8 fp32) += A (16x16 fp16, row-major) B (16x8 fp16, column-major)
+__device__ __forceinline__ void mma_16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 // ---------------------------------------------------------------------------
 // rows in
 // ---------------------------------------------------------------------------
@@ -39,145 +48,188 @@ struct Kv4AppendArgs {
   int tblocks;             // blocks per (b, head)
 };
 
-// D / 16 lanes hold a row, 16 elements each: two chunks of 8 that lie half a row apart, so that
-// both of a lane's 16-byte loads belong to whole lines of its row's lanes.
+// A warp takes 8 rows; lane (grp, tq) holds a quarter of row grp, D/4 elements, as pairs.  The rotation's bits of the element index divide between the tensor core and the
+// registers: bits 0, 1 and the two that name the lane's quarter are the 16 x 16 matrix H16, one
+// m16n8k16 MMA pair per 4 elements (whose operand is the row as it lies in memory, and whose result
+// has the same layout; half of its rows stay empty: two rows a lane took twice the registers and left
+// too few warps to keep the memory busy, 121 us for the case below); the others are additions between a lane's own pairs.  No shuffles, and a
+// fifth of the instructions of the stages as butterflies: append + read of 262144 rows of d = 128
+// took 122 us with those.
 template <int D>
-struct Kv4Row {
-  static constexpr int LANES = D / 16, ROWS = 32 / LANES;  // lanes per row, rows per warp
+struct Kv4Rows {
+  static constexpr int NE = D / 4, NP = NE / 2, BLOCKS = NE / 4;  // elements, pairs, groups of 4 of a lane and row
+  static constexpr int WARPS = 4;                                 // per CTA
+  static constexpr int RPL = 1, ROWS = 8 * RPL;                   // rows of a lane, of a warp
 };
 
-// y <- H y over the lanes of each row (element bits 0-2 in a chunk, then the lane's, then the
-// chunk), the stages in ascending order: the same additions whatever holds the row.
-template <int D>
-__device__ __forceinline__ void kv4_hadamard(float (&y)[16], int lane) {
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    const float p = y[i], q = y[i + 1];
-    y[i] = p + q;
-    y[i + 1] = p - q;
-  }
-  float2* const z = reinterpret_cast<float2*>(y);  // the other stages keep the pairs together
-#pragma unroll
-  for (int h = 1; h < 4; h <<= 1)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (!(i & h)) {
-        const float2 p = z[i], q = z[i + h];
-        z[i] = fadd2(p, q);
-        z[i + h] = fsub2(p, q);
-      }
-#pragma unroll
-  for (int h = 1; h < Kv4Row<D>::LANES; h <<= 1) {
-    const float sign = (lane & h) ? -1.f : 1.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      z[i] = ffma2(make_float2(sign, sign), z[i],
-                   make_float2(__shfl_xor_sync(0xffffffffu, z[i].x, h), __shfl_xor_sync(0xffffffffu, z[i].y, h)));
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = z[i], q = z[i + 4];
-    z[i] = fadd2(p, q);
-    z[i + 4] = fsub2(p, q);
-  }
+__device__ __forceinline__ void ld_global_32(const void* p, uint32_t* r) {
+  asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "l"(p));
 }
-__device__ __forceinline__ void kv4_unpack_bf16x8(const uint4& v, float* y) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// B operand of the H16 MMAs: entry (k, n) is (-1)^popc(k & n), n the column of half `nt`; the
+// second of each pair of k times `odd`
+__device__ __forceinline__ float kv4_h16(int k, int n) { return (__popc(k & n) & 1) ? -1.f : 1.f; }
+
+// The stages of H between a lane's groups of 4 elements.
+template <int D>
+__device__ __forceinline__ void kv4_hadamard_groups(float2 (&z)[Kv4Rows<D>::RPL][Kv4Rows<D>::NP]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y[2 * i] = __uint_as_float(w[i] << 16);
-    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int h = 1; h < Kv4Rows<D>::BLOCKS; h <<= 1)
+#pragma unroll
+    for (int b = 0; b < Kv4Rows<D>::BLOCKS; ++b)
+      if (!(b & h))
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
+            const float2 p = z[r][2 * b + x], q = z[r][2 * (b + h) + x];
+            z[r][2 * b + x] = fadd2(p, q);
+            z[r][2 * (b + h) + x] = fsub2(p, q);
+          }
+}
+// three-input maximum of magnitudes in which a NaN wins
+__device__ __forceinline__ float absmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
+}
+// sign bits of the pairs of a row: bits 15 and 31 of word i for elements 2 i and 2 i + 1
+template <int D>
+__device__ __forceinline__ void kv4_sign_masks(const float* signs, uint32_t* masks) {
+  for (int i = threadIdx.x; i < D / 2; i += 32 * Kv4Rows<D>::WARPS)
+    masks[i] = (signs && signs[2 * i] < 0.f ? 0x8000u : 0u) | (signs && signs[2 * i + 1] < 0.f ? 0x80000000u : 0u);
 }
 
 // blockIdx.y: keys, values.  What a row costs in instructions comes close to what it costs in
-// bytes: the quotient y / s is formed with the reciprocal, and only where it comes out next to the
-// border of two codes (an exact tie, often, as s and an unrotated y have 8 bits) by a division.
+// bytes: quotients are formed two at a time, and four codes are put together in the mantissa of one
+// fp32 number.  (The quotient has to be the rounded one: y / s is often an exact tie of two codes, as
+// s and an unrotated y have 8 bits.)
 template <int D>
-__global__ void __launch_bounds__(256) fa_kv4_append_kernel(const Kv4AppendArgs a) {
-  using R = Kv4Row<D>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % R::LANES;
+__global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS) fa_kv4_append_kernel(const Kv4AppendArgs a) {
+  using R = Kv4Rows<D>;
+  __shared__ __align__(16) uint32_t masks[D / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane >> 2, tq = lane & 3;
   const int bh = blockIdx.x / a.tblocks;
-  const int t = (blockIdx.x % a.tblocks) * (8 * R::ROWS) + warp * R::ROWS + lane / R::LANES;
-  const bool is_v = blockIdx.y == 1;
+  const int t0 = (blockIdx.x % a.tblocks) * (R::ROWS * R::WARPS) + warp * R::ROWS;
+  const bool is_v = blockIdx.y == 1, rotate = !is_v && a.signs;
+  if (rotate) {
+    kv4_sign_masks<D>(a.signs, masks);
+    __syncthreads();
+  }
   const int n_new = a.n_new ? min(a.n_new[bh], a.T) : a.T;
-  const long long bt = static_cast<long long>(bh) * a.T + t;
-  bool live = t < n_new;
-  int src = -1;
-  long long dst = -1;
-  if (live) {
-    src = a.rows ? a.rows[bt] : t;
-    dst = a.slots ? a.slots[bt] : (a.start ? static_cast<long long>(a.start[bh]) : 0) + t;
-    live = src >= 0 && src < a.N && dst >= 0 && dst < a.C;
-  }
-  __align__(8) float y[16];
-  uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-  if (live) {
-    const uint4* x = reinterpret_cast<const uint4*>((is_v ? a.v : a.k) + (static_cast<size_t>(bh) * a.N + src) * D);
-    v0 = x[sub];
-    v1 = x[sub + R::LANES];
-  }
-  kv4_unpack_bf16x8(v0, y);
-  kv4_unpack_bf16x8(v1, y + 8);
-  if (!is_v && a.signs) {
+  if (t0 >= n_new) return;
+  int src[R::RPL];
+  long long dst[R::RPL];
+  bool live[R::RPL];
+  uint32_t w[R::RPL][R::NP];  // the rows' pairs of bf16
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+  for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
+    const int t = t0 + grp + 8 * r;
+    const long long bt = static_cast<long long>(bh) * a.T + t;
+    live[r] = t < n_new;
+    src[r] = live[r] ? (a.rows ? a.rows[bt] : t) : -1;
+    dst[r] = live[r] ? (a.slots ? a.slots[bt] : (a.start ? static_cast<long long>(a.start[bh]) : 0) + t) : -1;
+    live[r] = src[r] >= 0 && src[r] < a.N && dst[r] >= 0 && dst[r] < a.C;
+    const __nv_bfloat16* x = (is_v ? a.v : a.k) + (static_cast<size_t>(bh) * a.N + (live[r] ? src[r] : 0)) * D + tq * 16;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[8 * c + i] *= a.signs[(sub + c * R::LANES) * 8 + i];
-    kv4_hadamard<D>(y, lane);
-  }
-  // the largest magnitude by its bits: an infinity or a NaN in the row wins
-  uint32_t top = 0;
+    for (int u = 0; u < D / 64; ++u) {
+      if (live[r]) ld_global_32(x + 64 * u, &w[r][8 * u]);
+      else
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
-#pragma unroll
-  for (int h = 1; h < R::LANES; h <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, h));
-  const bool finite = top < 0x7f800000u;
-  const __nv_bfloat16 sb = finite ? __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.f))
-                                  : __ushort_as_bfloat16(static_cast<unsigned short>(0x7fff));
-  const float s = __bfloat162float(sb);
-  // codes as the low bits of 1.5 2^23 + c + 8; |y| <= amax, so |c| <= 7 where s is a normal number
-  uint32_t packed[2] = {0u, 0u};
-  const float kMagic = 12582912.f;
-  if (finite && s >= 1e-30f) {
-    const float inv = __frcp_rn(s);
-    const float2 inv2 = make_float2(inv, inv), magic2 = make_float2(kMagic, kMagic);
-    float off = 0.f;
-    __align__(8) float u[16];
-    const float2* const z = reinterpret_cast<const float2*>(y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 q = fmul2(z[i], inv2), m = fadd2(q, magic2), r = fsub2(q, fsub2(m, magic2));
-      u[2 * i] = m.x, u[2 * i + 1] = m.y;
-      off = fmax3(off, fabsf(r.x), fabsf(r.y));
+        for (int i = 0; i < 8; ++i) w[r][8 * u + i] = 0u;
     }
-    if (off > 0.4999f) {
+  }
+  float2 z[R::RPL][R::NP];
+  if (rotate) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float q = y[i] * inv;
-        if (fabsf(q - (u[i] - kMagic)) > 0.4999f) u[i] = rintf(__fdiv_rn(y[i], s)) + kMagic;
+    for (int i = 0; i < R::NP; ++i) {
+      const uint32_t m = masks[32 * (i >> 3) + tq * 8 + (i & 7)];
+#pragma unroll
+      for (int r = 0; r < R::RPL; ++r) w[r][i] ^= m;
+    }
+    uint32_t b[2][2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int k8 = 0; k8 < 2; ++k8)
+        b[nt][k8] = pack_bf16x2(kv4_h16(2 * tq + 8 * k8, grp + 8 * nt), kv4_h16(2 * tq + 1 + 8 * k8, grp + 8 * nt));
+#pragma unroll
+    for (int g = 0; g < R::BLOCKS; ++g)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_16816(c, w[0][2 * g], 0u, w[0][2 * g + 1], 0u, b[nt][0], b[nt][1]);
+        z[0][2 * g + nt] = make_float2(c[0], c[1]);
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) packed[i >> 3] |= ((__float_as_uint(u[i]) + 8u) & 15u) << (4 * (i & 7));
+    kv4_hadamard_groups<D>(z);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float c = 0.f;
-      if (finite && s > 0.f) c = fminf(7.f, fmaxf(-7.f, rintf(__fdiv_rn(y[i], s))));
-      packed[i >> 3] |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * (i & 7));
-    }
+    for (int r = 0; r < Kv4Rows<D>::RPL; ++r)
+#pragma unroll
+      for (int i = 0; i < R::NP; ++i)
+        z[r][i] = make_float2(__uint_as_float(w[r][i] << 16), __uint_as_float(w[r][i] & 0xffff0000u));
   }
-  if (!live) return;
-  const size_t row = static_cast<size_t>(bh) * a.C + dst;
-  uint32_t* codes = reinterpret_cast<uint32_t*>((is_v ? a.vc : a.kc) + row * (D / 2));
-  codes[sub] = packed[0];
-  codes[sub + R::LANES] = packed[1];
-  if (sub == 0) {
-    (is_v ? a.vs : a.ks)[row] = sb;
-    if (!is_v) {
-      if (a.acc) a.acc[row] = a.w ? a.w[static_cast<size_t>(bh) * a.ldw + src] : 0.f;
-      if (a.pos) a.pos[row] = (a.base ? a.base[bh / a.Hkv] : 0) + src;
+#pragma unroll
+  for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < R::NP; ++i) top = absmax3_nan(top, z[r][i].x, z[r][i].y);
+    top = absmax3_nan(top, __shfl_xor_sync(0xffffffffu, top, 1), 0.f);
+    top = absmax3_nan(top, __shfl_xor_sync(0xffffffffu, top, 2), 0.f);
+    const bool finite = top < INFINITY;
+    const __nv_bfloat16 sb = finite ? __float2bfloat16_rn(__fdiv_rn(top, 7.f))
+                                    : __ushort_as_bfloat16(static_cast<unsigned short>(0x7fff));
+    const float s = __bfloat162float(sb);
+    float2 c[R::NP];  // the codes less 8, whole numbers
+    if (finite && s >= 1e-30f) {
+      // |y| <= amax, so |c| <= 7 where s is a normal number.  With the rounded reciprocal one step on
+      // the remainder (an fma) gives the correctly rounded quotient (Markstein; s has 8 bits).
+      const float inv = __frcp_rn(s), kMagic = 12582912.f;  // 1.5 2^23
+      const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-s, -s), magic2 = make_float2(kMagic, kMagic);
+#pragma unroll
+      for (int i = 0; i < R::NP; ++i) {
+        float2 q = fmul2(z[r][i], inv2);
+        q = ffma2(ffma2(q, neg2, z[r][i]), inv2, q);
+        c[i] = fsub2(fadd2(q, magic2), magic2);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R::NP; ++i) {
+        const bool some = finite && s > 0.f;
+        c[i].x = some ? fminf(7.f, fmaxf(-7.f, rintf(__fdiv_rn(z[r][i].x, s)))) : 0.f;
+        c[i].y = some ? fminf(7.f, fmaxf(-7.f, rintf(__fdiv_rn(z[r][i].y, s)))) : 0.f;
+      }
+    }
+    uint32_t packed[R::NE / 8];
+#pragma unroll
+    for (int i = 0; i < R::NE / 8; ++i) {
+      uint32_t half[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // c0 + 16 c1 + 256 c2 + 4096 c3, plus 0x8888, in the low bits of 2^23 + ...
+        const float2 t = ffma2(c[4 * i + 2 * h + 1], make_float2(256.f, 256.f), c[4 * i + 2 * h]);
+        half[h] = __float_as_uint(fmaf(t.y, 16.f, t.x) + (8388608.f + 34952.f));
+      }
+      packed[i] = __byte_perm(half[0], half[1], 0x5410);
+    }
+    if (!live[r]) continue;
+    const size_t row = static_cast<size_t>(bh) * a.C + dst[r];
+    uint8_t* codes = (is_v ? a.vc : a.kc) + row * (D / 2) + tq * 8;
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u) *reinterpret_cast<uint2*>(codes + 32 * u) = make_uint2(packed[2 * u], packed[2 * u + 1]);
+    if (tq == 0) {
+      (is_v ? a.vs : a.ks)[row] = sb;
+      if (!is_v) {
+        if (a.acc) a.acc[row] = a.w ? a.w[static_cast<size_t>(bh) * a.ldw + src[r]] : 0.f;
+        if (a.pos) a.pos[row] = (a.base ? a.base[bh / a.Hkv] : 0) + src[r];
+      }
     }
   }
 }
@@ -199,48 +251,117 @@ struct Kv4ReadArgs {
   int tblocks;
 };
 
-// The codes of a rotated row go back through H as whole numbers (sums of at most 256 codes,
-// exact in fp32): x = signs (s / d) H c, rounded once, to bf16.
+// The codes of a rotated row go back through H as whole numbers (exact in fp32): x = signs (s / d)
+// H c, rounded once, to bf16.  The nibbles n = c + 8 enter the MMAs as fp16 subnormals, n 2^-24 the
+// even ones and n 2^-20 the odd ones, against +-2^14 and +-2^10; H of the eights is 8 d in element 0
+// and nothing elsewhere.
 template <int D>
-__global__ void __launch_bounds__(256) fa_kv4_read_kernel(const Kv4ReadArgs a) {
-  using R = Kv4Row<D>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % R::LANES;
+__global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS) fa_kv4_read_kernel(const Kv4ReadArgs a) {
+  using R = Kv4Rows<D>;
+  __shared__ __align__(16) uint32_t masks[D / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane >> 2, tq = lane & 3;
   const int bh = blockIdx.x / a.tblocks;
-  const int t = (blockIdx.x % a.tblocks) * (8 * R::ROWS) + warp * R::ROWS + lane / R::LANES;
-  const bool is_v = blockIdx.y == 1;
-  const long long bt = static_cast<long long>(bh) * a.T + t;
+  const int t0 = (blockIdx.x % a.tblocks) * (R::ROWS * R::WARPS) + warp * R::ROWS;
+  const bool is_v = blockIdx.y == 1, rotate = !is_v && a.signs;
+  if (rotate) {
+    kv4_sign_masks<D>(a.signs, masks);
+    __syncthreads();
+  }
+  if (t0 >= a.T) return;
   const int len = a.lens ? min(a.lens[bh], a.C) : a.C;
-  long long r = -1;
-  if (t < a.T) r = a.slots ? a.slots[bt] : static_cast<long long>(a.first) + t;
-  const bool live = r >= 0 && r < len;
-  uint32_t w[2] = {0x88888888u, 0x88888888u};  // zeros
-  float s = 0.f;
-  if (live) {
-    const size_t row = static_cast<size_t>(bh) * a.C + r;
-    const uint32_t* codes = reinterpret_cast<const uint32_t*>((is_v ? a.vc : a.kc) + row * (D / 2));
-    w[0] = codes[sub];
-    w[1] = codes[sub + R::LANES];
-    s = __bfloat162float((is_v ? a.vs : a.ks)[row]);
+  uint32_t w[R::RPL][R::NE / 8];
+  float s[R::RPL];
+#pragma unroll
+  for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
+    const int t = t0 + grp + 8 * r;
+    long long at = -1;
+    if (t < a.T) at = a.slots ? a.slots[static_cast<long long>(bh) * a.T + t] : static_cast<long long>(a.first) + t;
+    const bool live = at >= 0 && at < len;
+    const size_t row = static_cast<size_t>(bh) * a.C + (live ? at : 0);
+    const uint8_t* codes = (is_v ? a.vc : a.kc) + row * (D / 2) + tq * 8;
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u) {
+      const uint2 v = *reinterpret_cast<const uint2*>(codes + 32 * u);
+      w[r][2 * u] = v.x, w[r][2 * u + 1] = v.y;
+    }
+    s[r] = __bfloat162float((is_v ? a.vs : a.ks)[row]);
+    if (!live) {  // zeros, whatever the row holds
+      s[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < R::NE / 8; ++i) w[r][i] = 0x88888888u;
+    }
   }
-  __align__(8) float y[16];
+  uint32_t x[R::RPL][R::NP];  // the rows' pairs of bf16
+  if (rotate) {
+    float2 z[R::RPL][R::NP];
+    uint32_t b[2][2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i)  // 2^23 + code, less 2^23 + 8
-    y[i] = __uint_as_float(0x4B000000u | ((w[i >> 3] >> (4 * (i & 7))) & 15u)) - 8388616.f;
-  if (!is_v && a.signs) {
-    kv4_hadamard<D>(y, lane);
-    s *= 1.f / D;
+    for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+      for (int k8 = 0; k8 < 2; ++k8) {
+        const float even = 16384.f * kv4_h16(2 * tq + 8 * k8, grp + 8 * nt);
+        const float odd = 1024.f * kv4_h16(2 * tq + 1 + 8 * k8, grp + 8 * nt);
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(b[nt][k8]) : "f"(odd), "f"(even));
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[8 * c + i] *= a.signs[(sub + c * R::LANES) * 8 + i];
+    for (int g = 0; g < R::BLOCKS; ++g) {
+      uint32_t p[R::RPL][2];  // bytes 2 g, 2 g + 1 of the lane's codes, a byte in each half
+#pragma unroll
+      for (int r = 0; r < Kv4Rows<D>::RPL; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          p[r][h] = __byte_perm(w[r][g >> 1], 0u, (g & 1) ? (h ? 0x4343 : 0x4242) : (h ? 0x4141 : 0x4040)) & 0x00f0000fu;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_16816_f16(c, p[0][0], 0u, p[0][1], 0u, b[nt][0], b[nt][1]);
+        z[0][2 * g + nt] = make_float2(c[0], c[1]);
+      }
+    }
+    kv4_hadamard_groups<D>(z);
+#pragma unroll
+    for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
+      if (tq == 0) z[r][0].x -= 8.f * D / 1024.f;
+      float f = s[r] * (1024.f / D);
+      if (s[r] > 1e30f) {  // the product of the factors could pass fp32's range
+        f = s[r];
+#pragma unroll
+        for (int i = 0; i < R::NP; ++i) z[r][i] = fmul2(z[r][i], make_float2(1024.f / D, 1024.f / D));
+      }
+#pragma unroll
+      for (int i = 0; i < R::NP; ++i) {
+        const float2 v = fmul2(z[r][i], make_float2(f, f));
+        x[r][i] = pack_bf16x2(v.x, v.y) ^ masks[32 * (i >> 3) + tq * 8 + (i & 7)];
+      }
+    }
+  } else {
+    // codes as bf16, (128 + n) - 136, times the scale: a product of 4 and 8 bits, rounded once
+#pragma unroll
+    for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
+      const uint32_t s2 = pack_bf16x2(s[r], s[r]);
+#pragma unroll
+      for (int i = 0; i < R::NE / 8; ++i) {
+        uint32_t v[4];  // elements (0, 4), (1, 5), (2, 6), (3, 7)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t n = ((w[r][i] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
+          asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(v[e]) : "r"(n), "r"(0xC308C308u));
+          asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v[e]) : "r"(v[e]), "r"(s2));
+        }
+        x[r][4 * i] = __byte_perm(v[0], v[1], 0x5410);
+        x[r][4 * i + 1] = __byte_perm(v[2], v[3], 0x5410);
+        x[r][4 * i + 2] = __byte_perm(v[0], v[1], 0x7632);
+        x[r][4 * i + 3] = __byte_perm(v[2], v[3], 0x7632);
+      }
+    }
   }
-  if (t >= a.T) return;
-  uint4* out = reinterpret_cast<uint4*>((is_v ? a.v : a.k) + bt * D);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const float* z = y + 8 * c;
-    out[sub + c * R::LANES] = make_uint4(pack_bf16x2(z[0] * s, z[1] * s), pack_bf16x2(z[2] * s, z[3] * s),
-                                         pack_bf16x2(z[4] * s, z[5] * s), pack_bf16x2(z[6] * s, z[7] * s));
+  for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
+    const int t = t0 + grp + 8 * r;
+    if (t >= a.T) continue;
+    __nv_bfloat16* out = (is_v ? a.v : a.k) + (static_cast<long long>(bh) * a.T + t) * D + tq * 16;
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u) st_global_32(out + 64 * u, &x[r][8 * u]);
   }
 }
 
@@ -327,14 +448,6 @@ struct Kv4Cfg {
   static_assert(STAGES >= 2 && BYTES <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ void mma_16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));

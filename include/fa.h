@@ -228,7 +228,8 @@ int fa_fwd_fp8_gqa(const void* q8, const void* k8, const void* v8, const float* 
  * order of positions.  Memory behind them is never written by these calls, and what it holds
  * never reaches a result.  All the int32 and fp32 arrays are device memory, read when the
  * kernel runs, so that a captured graph follows them.
- * Alignment: kc, ks, vc, vs, acc, pos, q, k, v, o 16 bytes, workspaces 256, others 4.
+ * Alignment: k and v of fa_kv4_append and fa_kv4_read 32 bytes; kc, ks, vc, vs, acc, pos, q, o
+ * and other k, v 16 bytes; workspaces 256; the rest 4.
  * Limits: C <= 2^30, d in {64, 128, 256}, and the limits above with C (and N, T) for N.
  * ------------------------------------------------------------------------- */
 

@@ -7,6 +7,7 @@ import torch
 
 vp, ci, cf, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 GOOD, ODD4, ODD8, ODD2 = vp(1 << 20), vp((1 << 20) + 4), vp((1 << 20) + 8), vp((1 << 20) + 2)
+ODD16 = vp((1 << 20) + 16)
 INVALID, UNSUPPORTED, ALIGNMENT = 1, 2, 3
 
 
@@ -32,6 +33,8 @@ def test_append(lib):
     for n in "k v kc ks vc vs".split():
         assert go(**{n: None}) == INVALID, n
         assert go(**{n: ODD8}) == ALIGNMENT, n
+    for n in "k v".split():
+        assert go(**{n: ODD16}) == ALIGNMENT, n     # read 32 bytes at a time
     for n in "acc pos".split():
         assert go(**{n: ODD4}) == ALIGNMENT, n
     for n in "signs w rows slots start n_new base".split():
@@ -55,6 +58,8 @@ def test_read(lib):
     for n in "kc ks vc vs k v".split():
         assert go(**{n: None}) == INVALID, n
         assert go(**{n: ODD8}) == ALIGNMENT, n
+    for n in "k v".split():
+        assert go(**{n: ODD16}) == ALIGNMENT, n
     for n in "signs slots lens".split():
         assert go(**{n: ODD2}) == ALIGNMENT, n
     assert go(T=0) == INVALID and go(first=-1) == INVALID and go(C=64) == INVALID
