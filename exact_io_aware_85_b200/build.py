@@ -15,6 +15,7 @@ LIB = os.path.join(PKG, "libfa.so")
 LIB_DEBUG = os.path.join(PKG, "libfa_debug.so")
 SOURCES = ["api.cu", "sm100.cuh", "fwd.cuh", "bwd.cuh", "fp8.cuh", "decode.cuh", "fwd256.cuh", "bwd256.cuh",
            "kv4.cuh", "evict.cuh", "key_weights.cuh", "api_cache.cuh"]
+CALL = os.path.join(PKG, "_fa_call.so")  # the cache operators' argument marshalling (csrc/call.cpp)
 HEADER = os.path.join(os.path.dirname(PKG), "include", "fa.h")
 
 
@@ -34,8 +35,31 @@ def needs_build(lib: str = LIB) -> bool:
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 
+def call_command(out: str = CALL):
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [sysconfig.get_paths()["include"], *cpp_extension.include_paths(device_type="cuda")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            *(f"-I{i}" for i in inc), os.path.join(CSRC, "call.cpp"), "-o", out, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+
+
+def build_call(force: bool = False) -> str:
+    src = os.path.join(CSRC, "call.cpp")
+    if force or not os.path.exists(CALL) or os.path.getmtime(src) > os.path.getmtime(CALL):
+        tmp = f"{CALL}.{os.getpid()}"
+        subprocess.run(call_command(tmp), check=True)
+        os.replace(tmp, CALL)
+    return CALL
+
+
 def build_library(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     out = LIB_DEBUG if debug else LIB
+    build_call(force)
     if force or needs_build(out):
         extra = (("-Xptxas", "-v") if verbose else ()) + (("-DFA_DEBUG",) if debug else ())
         subprocess.run(nvcc_command(out=out, extra=extra), check=True)

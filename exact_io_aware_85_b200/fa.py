@@ -19,6 +19,11 @@ if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{os.path.basename(_LIB_PATH)} is not built ({_LIB_PATH}); run "
                       f"`python -m exact_io_aware_85_b200.build{' --debug' if _DEBUG else ''}`")
 
+try:
+    from . import _fa_call  # argument marshalling of the cache operators
+except ImportError as e:
+    raise ImportError("_fa_call.so is not built; run `python -m exact_io_aware_85_b200.build`") from e
+
 lib = ctypes.CDLL(_LIB_PATH)
 _vp, _ci, _cf, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 lib.fa_fwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _ci, _cf, _vp]
@@ -295,30 +300,36 @@ lib.fa_decode_kv4_workspace_bytes.restype = _sz
 lib.fa_decode_kv4_workspace_bytes.argtypes = [_ci] * 6
 lib.fa_decode_kv4.argtypes = [_vp] * 10 + [_ci] * 5 + [_cf, _vp, _sz, _vp]
 _i32 = torch.int32
+_fa_call.bind(*(ctypes.cast(getattr(lib, name), _vp).value for name in (
+    "fa_key_weights", "fa_evict_keep", "fa_evict_slots", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4")))
 
 
-def _args(where: str, stream, *tensors):
-    """The stream's handle and the tensors' addresses (None for None) for a call of the
-    cache operators; `tensors` are (name, tensor, dtype, shape).  The checks are those of
-    _need, and that the tensors (and a given stream) belong to the current device, where
-    the kernels are launched.  These calls run once per decoded token and layer, so the
-    checks that pass cost little; one that fails is explained by _need."""
-    dev = torch.cuda.current_device()
-    ptrs = []
+def _done(status: int, where: str, *tensors) -> None:
+    """Ends a call of a cache operator, which _fa_call checks and makes (it takes the host a
+    quarter of what the checks take in Python): raises on a status, and explains a call that was
+    refused before the library saw it (status -1); `tensors` are (name, tensor, dtype, shape)."""
+    if status == FA_OK:
+        return
+    if status > 0:
+        _check(status, where)
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     for name, t, dtype, shape in tensors:
         if t is None:
-            ptrs.append(None)
             continue
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
-                and t.is_contiguous()):
-            _need(where, **{name: (t, dtype, shape)})
+        _need(where, **{name: (t, dtype, shape)})
+        if t.get_device() != dev:
             raise FAError(FA_ERR_INVALID_ARG, f"{where}({name}: on {t.device}, the current device is cuda:{dev})")
-        ptrs.append(t.data_ptr())
+    raise FAError(FA_ERR_INVALID_ARG, f"{where}: an argument is out of range")
+
+
+def _handle(where: str, stream):
+    """A given stream's handle; it has to belong to the current device, where the kernels run."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev), ptrs
-    if stream.device_index != dev:
-        raise FAError(FA_ERR_INVALID_ARG, f"{where}(stream: of cuda:{stream.device_index}, the current device is cuda:{dev})")
-    return stream.cuda_stream, ptrs
+        return None
+    if stream.device_index != torch.cuda.current_device():
+        raise FAError(FA_ERR_INVALID_ARG, f"{where}(stream: of cuda:{stream.device_index}, the current device is "
+                                          f"cuda:{torch.cuda.current_device()})")
+    return stream.cuda_stream
 
 
 def _required(where: str, **tensors) -> None:
@@ -343,43 +354,49 @@ def fa_key_weights(q, k, lse, w, causal: bool, scale: float, workspace, window=N
     """Attention weight that each key of a prompt received from the last `window` queries
     (None: all): w (fp32 [B, H_kv, >= N]) columns 0 .. N-1; lse is the forward's; n_rows:
     int32 [B] tokens of each sequence, or None."""
-    _required("fa_key_weights", q=q, k=k, lse=lse, w=w, workspace=workspace)
-    B, H, N, d = _dims(q)
-    Hkv = k.shape[1] if k.dim() == 4 else -1
-    ldw = w.shape[-1] if w.dim() == 3 else -1
-    s, p = _args("fa_key_weights", stream, ("q", q, _bf, (B, H, N, d)), ("k", k, _bf, (B, Hkv, N, d)),
-                 ("lse", lse, _f32, (B, H, N)), ("w", w, _f32, (B, Hkv, ldw)), ("n_rows", n_rows, _i32, (B,)),
-                 ("workspace", workspace, _u8, (workspace.numel(),)))
-    _check(lib.fa_key_weights(*p[:5], B, H, Hkv, N, ldw, d, int(causal), N if window is None else int(window),
-                              float(scale), p[5], workspace.numel(), s), "fa_key_weights")
+    where = "fa_key_weights"
+    st = _fa_call.key_weights(q, k, lse, w, n_rows, workspace, causal, window, scale, _handle(where, stream))
+    if st:
+        if st < 0:
+            _required(where, q=q, k=k, lse=lse, w=w, workspace=workspace)
+        B, H, N, d = _dims(q)
+        Hkv = k.shape[1] if k.dim() == 4 else -1
+        ldw = w.shape[-1] if w.dim() == 3 else -1
+        _done(st, where, ("q", q, _bf, (B, H, N, d)), ("k", k, _bf, (B, Hkv, N, d)), ("lse", lse, _f32, (B, H, N)),
+              ("w", w, _f32, (B, Hkv, ldw)), ("n_rows", n_rows, _i32, (B,)),
+              ("workspace", workspace, _u8, (workspace.numel(),)))
 
 
 def fa_evict_keep(w, idx, count, n_recent: int, n_sink: int, lens=None, stream=None) -> None:
     """The idx.shape[-1] rows of each head that stay, by weight: idx (int32 [B, H_kv, keep],
     ascending, -1 behind), count (int32 [B, H_kv]); w: fp32 [B, H_kv, C]; lens: int32 [B, H_kv]
     rows in use, or None (C)."""
-    _required("fa_evict_keep", w=w, idx=idx, count=count)
-    if w.dim() != 3 or idx.dim() != 3:
-        raise FAError(FA_ERR_INVALID_ARG, "fa_evict_keep(w: expected [B, H_kv, C], idx: [B, H_kv, keep])")
-    B, Hkv, C = w.shape
-    keep = idx.shape[2]
-    s, p = _args("fa_evict_keep", stream, ("w", w, _f32, (B, Hkv, C)), ("lens", lens, _i32, (B, Hkv)),
-                 ("idx", idx, _i32, (B, Hkv, keep)), ("count", count, _i32, (B, Hkv)))
-    _check(lib.fa_evict_keep(*p, B, Hkv, C, keep, int(n_recent), int(n_sink), s), "fa_evict_keep")
+    where = "fa_evict_keep"
+    st = _fa_call.evict_keep(w, lens, idx, count, n_recent, n_sink, _handle(where, stream))
+    if st:
+        if st < 0:
+            _required(where, w=w, idx=idx, count=count)
+            if w.dim() != 3 or idx.dim() != 3:
+                raise FAError(FA_ERR_INVALID_ARG, f"{where}(w: expected [B, H_kv, C], idx: [B, H_kv, keep])")
+        (B, Hkv, C), keep = w.shape, idx.shape[2]
+        _done(st, where, ("w", w, _f32, (B, Hkv, C)), ("lens", lens, _i32, (B, Hkv)), ("idx", idx, _i32, (B, Hkv, keep)),
+              ("count", count, _i32, (B, Hkv)))
 
 
 def fa_evict_slots(acc, pos, lens, seen, slots, budget: int, n_recent: int, n_sink: int, stream=None) -> None:
     """The rows that slots.shape[-1] new tokens take in each head: free rows, then the lightest
     of the rows in use; lens is updated.  acc: fp32, pos: int32 [B, H_kv, C]; lens: int32
     [B, H_kv]; seen: int32 [B] tokens seen so far; slots: int32 [B, H_kv, T]."""
-    _required("fa_evict_slots", acc=acc, pos=pos, lens=lens, seen=seen, slots=slots)
-    if acc.dim() != 3 or slots.dim() != 3:
-        raise FAError(FA_ERR_INVALID_ARG, "fa_evict_slots(acc: expected [B, H_kv, C], slots: [B, H_kv, T])")
-    B, Hkv, C = acc.shape
-    T = slots.shape[2]
-    s, p = _args("fa_evict_slots", stream, ("acc", acc, _f32, (B, Hkv, C)), ("pos", pos, _i32, (B, Hkv, C)),
-                 ("lens", lens, _i32, (B, Hkv)), ("seen", seen, _i32, (B,)), ("slots", slots, _i32, (B, Hkv, T)))
-    _check(lib.fa_evict_slots(*p, B, Hkv, C, int(budget), T, int(n_recent), int(n_sink), s), "fa_evict_slots")
+    where = "fa_evict_slots"
+    st = _fa_call.evict_slots(acc, pos, lens, seen, slots, budget, n_recent, n_sink, _handle(where, stream))
+    if st:
+        if st < 0:
+            _required(where, acc=acc, pos=pos, lens=lens, seen=seen, slots=slots)
+            if acc.dim() != 3 or slots.dim() != 3:
+                raise FAError(FA_ERR_INVALID_ARG, f"{where}(acc: expected [B, H_kv, C], slots: [B, H_kv, T])")
+        (B, Hkv, C), T = acc.shape, slots.shape[2]
+        _done(st, where, ("acc", acc, _f32, (B, Hkv, C)), ("pos", pos, _i32, (B, Hkv, C)), ("lens", lens, _i32, (B, Hkv)),
+              ("seen", seen, _i32, (B,)), ("slots", slots, _i32, (B, Hkv, T)))
 
 
 def fa_kv4_append(k, v, kc, ks, vc, vs, signs=None, rows=None, slots=None, start=None, n_new=None, w=None, acc=None,
@@ -388,35 +405,39 @@ def fa_kv4_append(k, v, kc, ks, vc, vs, signs=None, rows=None, slots=None, start
     [B, H_kv, C, d / 2]; ks, vs: bf16 [B, H_kv, C]): source rows `rows` (int32 [B, H_kv, T], None:
     0 .. N-1) to cache rows `slots` (int32 [B, H_kv, T]) or start + t (int32 [B, H_kv], None: 0)."""
     where = "fa_kv4_append"
-    _required(where, k=k, v=v, ks=ks, vc=vc, vs=vs)
-    B, Hkv, C, d = _cache_dims(where, kc)
-    N = k.shape[2] if k.dim() == 4 else -1
-    for given in (rows, slots):
-        if given is not None and (not isinstance(given, torch.Tensor) or given.dim() != 3):
-            raise FAError(FA_ERR_INVALID_ARG, f"{where}(rows, slots: expected int32 [B, H_kv, T])")
-    T = rows.shape[2] if rows is not None else slots.shape[2] if slots is not None else N
-    ldw = w.shape[-1] if isinstance(w, torch.Tensor) and w.dim() == 3 else 0
-    s, p = _args(where, stream, ("k", k, _bf, (B, Hkv, N, d)), ("v", v, _bf, (B, Hkv, N, d)),
-                 ("signs", signs, _f32, (d,)), ("w", w, _f32, (B, Hkv, ldw)), ("rows", rows, _i32, (B, Hkv, T)),
-                 ("slots", slots, _i32, (B, Hkv, T)), ("start", start, _i32, (B, Hkv)), ("n_new", n_new, _i32, (B, Hkv)),
-                 ("base", base, _i32, (B,)), ("kc", kc, _u8, (B, Hkv, C, d // 2)), ("ks", ks, _bf, (B, Hkv, C)),
-                 ("vc", vc, _u8, (B, Hkv, C, d // 2)), ("vs", vs, _bf, (B, Hkv, C)), ("acc", acc, _f32, (B, Hkv, C)),
-                 ("pos", pos, _i32, (B, Hkv, C)))
-    _check(lib.fa_kv4_append(*p, B, Hkv, N, T, C, ldw, d, s), where)
+    st = _fa_call.kv4_append(k, v, signs, w, rows, slots, start, n_new, base, kc, ks, vc, vs, acc, pos,
+                             _handle(where, stream))
+    if st:
+        if st < 0:
+            _required(where, k=k, v=v, ks=ks, vc=vc, vs=vs)
+        B, Hkv, C, d = _cache_dims(where, kc)
+        N = k.shape[2] if k.dim() == 4 else -1
+        for given in (rows, slots):
+            if given is not None and (not isinstance(given, torch.Tensor) or given.dim() != 3):
+                raise FAError(FA_ERR_INVALID_ARG, f"{where}(rows, slots: expected int32 [B, H_kv, T])")
+        T = rows.shape[2] if rows is not None else slots.shape[2] if slots is not None else N
+        ldw = w.shape[-1] if isinstance(w, torch.Tensor) and w.dim() == 3 else 0
+        _done(st, where, ("k", k, _bf, (B, Hkv, N, d)), ("v", v, _bf, (B, Hkv, N, d)), ("signs", signs, _f32, (d,)),
+              ("w", w, _f32, (B, Hkv, ldw)), ("rows", rows, _i32, (B, Hkv, T)), ("slots", slots, _i32, (B, Hkv, T)),
+              ("start", start, _i32, (B, Hkv)), ("n_new", n_new, _i32, (B, Hkv)), ("base", base, _i32, (B,)),
+              ("kc", kc, _u8, (B, Hkv, C, d // 2)), ("ks", ks, _bf, (B, Hkv, C)), ("vc", vc, _u8, (B, Hkv, C, d // 2)),
+              ("vs", vs, _bf, (B, Hkv, C)), ("acc", acc, _f32, (B, Hkv, C)), ("pos", pos, _i32, (B, Hkv, C)))
 
 
 def fa_kv4_read(kc, ks, vc, vs, k, v, signs=None, slots=None, first: int = 0, lens=None, stream=None) -> None:
     """The values that cache rows `slots` (int32 [B, H_kv, T]), or first + t, stand for: k, v
     (bf16 [B, H_kv, T, d]); zeros for rows outside 0 .. lens-1."""
     where = "fa_kv4_read"
-    _required(where, ks=ks, vc=vc, vs=vs, k=k, v=v)
-    B, Hkv, C, d = _cache_dims(where, kc)
-    T = k.shape[2] if k.dim() == 4 else -1
-    s, p = _args(where, stream, ("kc", kc, _u8, (B, Hkv, C, d // 2)), ("ks", ks, _bf, (B, Hkv, C)),
-                 ("vc", vc, _u8, (B, Hkv, C, d // 2)), ("vs", vs, _bf, (B, Hkv, C)), ("signs", signs, _f32, (d,)),
-                 ("slots", slots, _i32, (B, Hkv, T)), ("lens", lens, _i32, (B, Hkv)), ("k", k, _bf, (B, Hkv, T, d)),
-                 ("v", v, _bf, (B, Hkv, T, d)))
-    _check(lib.fa_kv4_read(*p, B, Hkv, T, C, int(first), d, s), where)
+    st = _fa_call.kv4_read(kc, ks, vc, vs, signs, slots, lens, k, v, first, _handle(where, stream))
+    if st:
+        if st < 0:
+            _required(where, ks=ks, vc=vc, vs=vs, k=k, v=v)
+        B, Hkv, C, d = _cache_dims(where, kc)
+        T = k.shape[2] if k.dim() == 4 else -1
+        _done(st, where, ("kc", kc, _u8, (B, Hkv, C, d // 2)), ("ks", ks, _bf, (B, Hkv, C)),
+              ("vc", vc, _u8, (B, Hkv, C, d // 2)), ("vs", vs, _bf, (B, Hkv, C)), ("signs", signs, _f32, (d,)),
+              ("slots", slots, _i32, (B, Hkv, T)), ("lens", lens, _i32, (B, Hkv)), ("k", k, _bf, (B, Hkv, T, d)),
+              ("v", v, _bf, (B, Hkv, T, d)))
 
 
 def fa_decode_kv4_workspace_bytes(B: int, H: int, H_kv: int, C: int, d: int, weights: bool) -> int:
@@ -428,12 +449,13 @@ def fa_decode_kv4(q, kc, ks, vc, vs, lens, o, lse, scale: float, workspace, sign
     """One decoding step over a 4-bit cache: q, o: bf16 [B, H, d]; lse: fp32 [B, H]; lens: int32
     [B, H_kv]; acc (fp32 [B, H_kv, C] or None) gets each row's softmax weight added."""
     where = "fa_decode_kv4"
-    _required(where, q=q, ks=ks, vc=vc, vs=vs, lens=lens, o=o, lse=lse, workspace=workspace)
-    B, Hkv, C, d = _cache_dims(where, kc)
-    H = q.shape[1] if q.dim() == 3 else -1
-    n_ws = workspace.numel()
-    s, p = _args(where, stream, ("q", q, _bf, (B, H, d)), ("kc", kc, _u8, (B, Hkv, C, d // 2)),
-                 ("ks", ks, _bf, (B, Hkv, C)), ("vc", vc, _u8, (B, Hkv, C, d // 2)), ("vs", vs, _bf, (B, Hkv, C)),
-                 ("signs", signs, _f32, (d,)), ("lens", lens, _i32, (B, Hkv)), ("o", o, _bf, (B, H, d)),
-                 ("lse", lse, _f32, (B, H)), ("acc", acc, _f32, (B, Hkv, C)), ("workspace", workspace, _u8, (n_ws,)))
-    _check(lib.fa_decode_kv4(*p[:10], B, H, Hkv, C, d, float(scale), p[10], n_ws, s), where)
+    st = _fa_call.decode_kv4(q, kc, ks, vc, vs, signs, lens, o, lse, acc, workspace, scale, _handle(where, stream))
+    if st:
+        if st < 0:
+            _required(where, q=q, ks=ks, vc=vc, vs=vs, lens=lens, o=o, lse=lse, workspace=workspace)
+        B, Hkv, C, d = _cache_dims(where, kc)
+        H = q.shape[1] if q.dim() == 3 else -1
+        _done(st, where, ("q", q, _bf, (B, H, d)), ("kc", kc, _u8, (B, Hkv, C, d // 2)), ("ks", ks, _bf, (B, Hkv, C)),
+              ("vc", vc, _u8, (B, Hkv, C, d // 2)), ("vs", vs, _bf, (B, Hkv, C)), ("signs", signs, _f32, (d,)),
+              ("lens", lens, _i32, (B, Hkv)), ("o", o, _bf, (B, H, d)), ("lse", lse, _f32, (B, H)),
+              ("acc", acc, _f32, (B, Hkv, C)), ("workspace", workspace, _u8, (workspace.numel(),)))
