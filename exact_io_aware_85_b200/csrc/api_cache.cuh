@@ -66,18 +66,25 @@ int launch_after(void (*kern)(Params...), dim3 grid, dim3 block, cudaStream_t s,
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
-template <int D, int NT>
-int launch_kv4_decode(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
+template <int D, int NT, bool TWO>
+int launch_kv4_decode_as(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
   using L = fa::Kv4Cfg<D, NT>;
-  auto kern = fa::fa_kv4_decode_kernel<D, NT>;
+  auto kern = fa::fa_kv4_decode_kernel<D, NT, TWO>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
   kern<<<a.grid, L::THREADS, L::BYTES, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
-  const int chunk = 1024;
-  return launch_after(fa::fa_kv4_combine_kernel<D, NT>, dim3(a.acc ? (a.C + chunk - 1) / chunk : 1, a.BHkv), dim3(256), s,
-                      a, chunk);
+  constexpr int KEYS = 4;
+  const int chunks = a.acc ? (a.C + 256 * KEYS - 1) / (256 * KEYS) : 1;
+  return launch_after(fa::fa_kv4_combine_kernel<D, NT, KEYS>, dim3(chunks, a.BHkv), dim3(256), s, a);
+}
+
+template <int D>
+int launch_kv4_decode(const fa::Kv4DecodeArgs& a, int nt, cudaStream_t s) {
+  const bool two = a.signs && (a.g > 4);
+  if (nt == 1) return two ? launch_kv4_decode_as<D, 1, true>(a, s) : launch_kv4_decode_as<D, 1, false>(a, s);
+  return two ? launch_kv4_decode_as<D, 2, true>(a, s) : launch_kv4_decode_as<D, 2, false>(a, s);
 }
 
 // The key weights' plan: CTAs, and the workspace's parts in bytes.
@@ -365,9 +372,9 @@ int fa_decode_kv4(const void* q, const void* kc, const void* ks, const void* vc,
   a.scores = acc ? reinterpret_cast<float*>(ws + p.scores) : nullptr;
   a.scale_log2 = scale * 1.4426950408889634f / (signs ? static_cast<float>(d) : 1.f);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 64) return p.nt == 1 ? launch_kv4_decode<64, 1>(a, s) : launch_kv4_decode<64, 2>(a, s);
-  if (d == 128) return p.nt == 1 ? launch_kv4_decode<128, 1>(a, s) : launch_kv4_decode<128, 2>(a, s);
-  return p.nt == 1 ? launch_kv4_decode<256, 1>(a, s) : launch_kv4_decode<256, 2>(a, s);
+  if (d == 64) return launch_kv4_decode<64>(a, p.nt, s);
+  if (d == 128) return launch_kv4_decode<128>(a, p.nt, s);
+  return launch_kv4_decode<256>(a, p.nt, s);
 }
 
 }  // extern "C"

@@ -467,7 +467,9 @@ struct Kv4Cursor {
   int bh, blk, nblk, len;
 };
 
-template <int D, int NT>
+// NT: 8-wide tiles of query heads; TWO: the second halves of a rotated q have MMAs of their own
+// (otherwise, for at most four heads, they sit in the unused columns).
+template <int D, int NT, bool TWO>
 __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kernel(const Kv4DecodeArgs a) {
   using L = Kv4Cfg<D, NT>;
   constexpr int NW = L::NW, ST = L::STAGES, NQ = 8 * NT, WORKERS = NW * 32;
@@ -578,8 +580,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
 
   const int g = a.g;
   const bool rotated = a.signs != nullptr;
-  const bool dup = NT == 1 && rotated && g <= 4;  // second halves of q in columns 4-7
-  const bool two = rotated && !dup;
+  const bool dup = !TWO && rotated;  // second halves of q in columns 4-7
   constexpr int EPL = D / 4 < 32 ? D / 4 : 32;    // elements of a lane's chunk of a key
   constexpr float kTwo24 = 16777216.f;
   bool ok = true;
@@ -644,7 +645,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
         const int nt = n >> 3, col = n & 7;
         qf[((((nt * 2) * L::KSTEPS + ks) * 32 + col * 4 + ql) << 2) + sub] = hi;
         if (rotated) {
-          if (dup) qf[((ks * 32 + (col + 4) * 4 + ql) << 2) + sub] = lo;
+          if (!TWO) qf[((ks * 32 + (col + 4) * 4 + ql) << 2) + sub] = lo;
           else qf[((((nt * 2 + 1) * L::KSTEPS + ks) * 32 + col * 4 + ql) << 2) + sub] = lo;
         }
       }
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
                 const uint2 b = qfrag[((j * 2) * L::KSTEPS + ks) * 32];
                 mma_16816_f16(x[0][j], lo[0], lo[1], hi[0], hi[1], b.x, b.y);
                 mma_16816_f16(x[1][j], lo[2], lo[3], hi[2], hi[3], b.x, b.y);
-                if (two) {
+                if constexpr (TWO) {
                   const uint2 b2 = qfrag[((j * 2 + 1) * L::KSTEPS + ks) * 32];
                   mma_16816_f16(x[0][j], lo[0], lo[1], hi[0], hi[1], b2.x, b2.y);
                   mma_16816_f16(x[1][j], lo[2], lo[3], hi[2], hi[3], b2.x, b2.y);
@@ -965,15 +966,39 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
 }
 
 // Joins the parts of a head by their maxima: O, LSE, and each key's weight summed over the
-// query heads that share it.  grid (key chunks, B*Hkv).
-template <int D, int NT>
-__global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs a, int chunk) {
-  constexpr int NQ = 8 * NT, MT = D / 16;
+// query heads that share it.  grid (key chunks of 4 KEYS x 256, B*Hkv); the scores of a thread's
+// keys are on their way while the heads' LSE is put together.
+template <int D, int NT, int KEYS>
+__global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs a) {
+  constexpr int NQ = 8 * NT, MT = D / 16, CHUNK = 256 * KEYS;
   __shared__ float lse2[NQ];
-  const int bh = blockIdx.y, g = a.g, tid = threadIdx.x;
+  const int bh = blockIdx.y, g = a.g, tid = threadIdx.x, gp = a.gp;
   const int len = kv4_len(a.lens, bh, a.C);
-  if (blockIdx.x > 0 && blockIdx.x * chunk >= len) return;
+  const int key0 = blockIdx.x * CHUNK + tid;
+  if (blockIdx.x > 0 && blockIdx.x * CHUNK >= len) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const size_t row = static_cast<size_t>(bh) * a.C + key0;
+  float old[KEYS];
+  float2 sc[KEYS][2];  // the first four heads' scores
+  if (a.acc) {
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) {
+      const bool in = key0 + 256 * i < len;
+      old[i] = in ? a.acc[row + 256 * i] : 0.f;
+      sc[i][0] = sc[i][1] = make_float2(-INFINITY, -INFINITY);
+      if (in) {
+        const float* p = a.scores + (row + 256 * i) * gp;
+        if (gp == 1) sc[i][0].x = p[0];
+        else if ((gp & 3) == 0) {
+          const float4 v = *reinterpret_cast<const float4*>(p);
+          sc[i][0] = make_float2(v.x, v.y), sc[i][1] = make_float2(v.z, v.w);
+        } else {
+          sc[i][0] = *reinterpret_cast<const float2*>(p);
+          if (gp > 2) sc[i][1] = *reinterpret_cast<const float2*>(p + 2);
+        }
+      }
+    }
+  }
   // the CTAs that worked on this head
   const long long total = a.first[a.BHkv], b0 = a.first[bh], b1 = a.first[bh + 1];
   int i0 = 0, i1 = -1;
@@ -991,7 +1016,8 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
       L = L * ex2_approx(M - m_new) + p.y * ex2_approx(p.x - m_new);
       M = m_new;
     }
-    lse2[tid] = len > 0 ? M + log2f(L) : -INFINITY;
+    // heads that are not there weigh nothing
+    lse2[tid] = tid >= g ? INFINITY : len > 0 ? M + log2f(L) : -INFINITY;
     if (blockIdx.x == 0 && tid < g) a.lse[static_cast<size_t>(bh) * g + tid] = lse2[tid] * 0.69314718055994530942f;
   }
   __syncthreads();
@@ -1024,35 +1050,25 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
       }
     }
   if (a.acc) {
-    // four keys of a thread at a time, so that their loads are under way together
-    const int gp = a.gp, end = min(len, (blockIdx.x + 1) * chunk);
-    for (int key = blockIdx.x * chunk + tid; key < end; key += 1024) {
-      float w[4], old[4];
-      const size_t row = static_cast<size_t>(bh) * a.C + key;
+    float w[KEYS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = 0.f;
-        old[i] = key + 256 * i < end ? a.acc[row + 256 * i] : 0.f;
-      }
-      if (gp == 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (key + 256 * i < end) w[i] = ex2_approx(a.scores[row + 256 * i] - lse2[0]);
-      } else {
-        for (int h = 0; h < g; h += 2) {
-          const float l0 = lse2[h], l1 = h + 1 < g ? lse2[h + 1] : INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (key + 256 * i < end) {
-              const float2 v = *reinterpret_cast<const float2*>(a.scores + (row + 256 * i) * gp + h);
-              w[i] += ex2_approx(v.x - l0) + (h + 1 < g ? ex2_approx(v.y - l1) : 0.f);
-            }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (key + 256 * i < end) a.acc[row + 256 * i] = old[i] + w[i];
+    for (int i = 0; i < KEYS; ++i) {
+      w[i] = ex2_approx(sc[i][0].x - lse2[0]);
+      if (gp > 1) w[i] += ex2_approx(sc[i][0].y - lse2[1]);
+      if (gp > 2) w[i] += ex2_approx(sc[i][1].x - lse2[2]) + ex2_approx(sc[i][1].y - lse2[3]);
     }
+    for (int h = 4; h < g; h += 2) {
+      const float l0 = lse2[h], l1 = lse2[h + 1];
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i)
+        if (key0 + 256 * i < len) {
+          const float2 v = *reinterpret_cast<const float2*>(a.scores + (row + 256 * i) * gp + h);
+          w[i] += ex2_approx(v.x - l0) + ex2_approx(v.y - l1);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i)
+      if (key0 + 256 * i < len) a.acc[row + 256 * i] = old[i] + w[i];
   }
 }
 
