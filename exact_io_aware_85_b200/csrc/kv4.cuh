@@ -392,8 +392,9 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS) fa_kv4_read_kernel(con
 //     bf16 query is exact; a rotated query is held as a sum of two fp16 numbers (22 bits).  With
 //     at most four heads the second number sits in the MMA's unused columns.
 //   * P times the row's scale, u = p vs, meets V's codes in fp16 too (11 bits, so its rounding
-//     stays below that of the bf16 output).  Its range: u is held relative to 2^R, a running
-//     maximum of u like m of the scores, so what flushes is 2^-24 of the largest.
+//     stays below that of the bf16 output).  Its range: p = 2^(x - R) with R a running maximum of
+//     x + log2 vs instead of x, so that u stays near one and what flushes is 2^-24 of the largest;
+//     the softmax's sum is held relative to the same R.
 //   * Work is one list of blocks over all heads' lengths, cut into equal parts, one per CTA:
 //     ragged batches fill the GPU evenly.
 struct Kv4DecodeArgs {
@@ -408,10 +409,12 @@ struct Kv4DecodeArgs {
   float* lse;              // [B*H]
   float* acc;              // [B*Hkv, C] or null
   float* part_o;           // [grid + B*Hkv, 8 NT d]: slot (CTA + head), in the merge's fragment order
-  float* part_ml;          // [grid + B*Hkv, 8 NT, 4]: m, l, R
+  float2* part_rl;         // [grid + B*Hkv, 8 NT]: R, l
+  float* fac;              // [B*Hkv, 8 NT]: factors of the scores
   int* first;              // [B*Hkv + 1]: blocks before each head
-  float* scores;           // [B*Hkv, C, gp] in log2 units, or null
+  float* scores;           // [B*Hkv, C, gp]: log2 scores less their head's factor, or null
   int C, BHkv, g, gp, grid;
+  int stream;              // the cache is larger than the L2
   float scale_log2;        // softmax scale * log2(e), / d when rotated
 };
 
@@ -440,8 +443,10 @@ struct Kv4Cfg {
   static constexpr int OFF_RED = OFF_Q;                      // the merge's buffer lies over them
   static constexpr int Q_BYTES = NT * 2 * KSTEPS * 32 * 8;
   static constexpr int RED_BYTES = NW * MC * NT * 32 * 16;
-  static constexpr int OFF_ML = OFF_Q + (Q_BYTES > RED_BYTES ? Q_BYTES : RED_BYTES);  // [3][NW][8 NT]
-  static constexpr int OFF_FAC = OFF_ML + 3 * NW * 8 * NT * 4;  // [2][8 NT]
+  static constexpr int OFF_ML = OFF_Q + (Q_BYTES > RED_BYTES ? Q_BYTES : RED_BYTES);  // [2][NW][8 NT]
+  static constexpr int OFF_QRAW = OFF_ML + 2 * NW * 8 * NT * 4;  // bf16 [8 NT][D]: the next head's q
+  static constexpr int OFF_SIGN = OFF_QRAW + 8 * NT * D * 2;     // float [D]
+  static constexpr int OFF_FAC = OFF_SIGN + D * 4;               // [2][8 NT]
   static constexpr int OFF_BAR = OFF_FAC + 2 * 8 * NT * 4;
   static constexpr int OFF_MISC = OFF_BAR + 2 * STAGES * 8;
   static constexpr int BYTES = OFF_MISC + 256;
@@ -461,6 +466,27 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float bf16_bits_to_float(unsigned short u) {
   return __uint_as_float(static_cast<uint32_t>(u) << 16);
 }
+
+// bulk load whose lines are the first to leave the L2
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Position in the list of blocks: a head, a block of it, and the head's length.
 struct Kv4Cursor {
@@ -482,9 +508,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
   volatile int* const abort_sh = reinterpret_cast<volatile int*>(smem + L::OFF_MISC);
   int* const scan = reinterpret_cast<int*>(smem + L::OFF_MISC + 16);  // [NW + 1 + 2]
   float* const fac_sh = reinterpret_cast<float*>(smem + L::OFF_FAC);  // [NQ] factors, [NQ] accumulator starts
-  float* const wm = reinterpret_cast<float*>(smem + L::OFF_ML);       // [NW][NQ] each
-  float* const wl = wm + NW * NQ;
+  float* const wl = reinterpret_cast<float*>(smem + L::OFF_ML);       // [NW][NQ] each
   float* const wr = wl + NW * NQ;
+  __nv_bfloat16* const qraw = reinterpret_cast<__nv_bfloat16*>(smem + L::OFF_QRAW);
+  float* const sign_sh = reinterpret_cast<float*>(smem + L::OFF_SIGN);
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) {
     *abort_sh = 0;
@@ -552,9 +579,30 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
     } while (cur.nblk == 0);
   };
 
+  // A head's query comes by asynchronous copies well before its first block: with the ring full of
+  // copies a load waits its turn behind them for microseconds.
+  const int g = a.g;
+  auto fetch_q = [&](int bh) {
+    for (int i = tid; i < g * D / 8; i += WORKERS)
+      cp_async_16(qraw + 8 * i, a.q + static_cast<size_t>(bh) * g * D + 8 * i);
+  };
+  if (warp < NW) {
+    fetch_q(cur.bh);
+    if (a.signs)
+      for (int i = tid; i < D; i += WORKERS) cp_async_4(sign_sh + i, a.signs + i);
+  }
+  __syncthreads();
+
   if (warp == NW) {
     // ================= the loading warp: one thread, block after block ======================
     if (lane == 0) {
+      // The codes are read once a step; where all of them pass through the L2, they would take the
+      // scores' place there, which the second kernel reads.
+      const uint64_t policy = evict_first_policy();
+      auto load = [&](void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+        if (a.stream) bulk_load_hint(dst, src, bytes, bar, policy);
+        else bulk_load(dst, src, bytes, bar);
+      };
       int t = 0;
       while (true) {
         const int s = t % ST;
@@ -564,10 +612,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
         uint8_t* st = smem + s * L::STAGE;
         const size_t row = static_cast<size_t>(cur.bh) * a.C + key0;
         mbar_arrive_expect_tx(&full[s], rows * (2 * L::ROW + 4));
-        bulk_load(st, a.kc + row * L::ROW, rows * L::ROW, &full[s]);
-        bulk_load(st + L::OFF_KS, a.ks + row, rows * 2, &full[s]);
-        bulk_load(st + L::OFF_V, a.vc + row * L::ROW, rows * L::ROW, &full[s]);
-        bulk_load(st + L::OFF_VS, a.vs + row, rows * 2, &full[s]);
+        load(st, a.kc + row * L::ROW, rows * L::ROW, &full[s]);
+        load(st + L::OFF_KS, a.ks + row, rows * 2, &full[s]);
+        load(st + L::OFF_V, a.vc + row * L::ROW, rows * L::ROW, &full[s]);
+        load(st + L::OFF_VS, a.vs + row, rows * 2, &full[s]);
         ++t;
         if (--left == 0) break;
         if (++cur.blk == cur.nblk) next_head();
@@ -578,7 +626,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
     return;
   }
 
-  const int g = a.g;
   const bool rotated = a.signs != nullptr;
   const bool dup = !TWO && rotated;  // second halves of q in columns 4-7
   constexpr int EPL = D / 4 < 32 ? D / 4 : 32;    // elements of a lane's chunk of a key
@@ -595,16 +642,17 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
     __half* const qf = reinterpret_cast<__half*>(smem + L::OFF_Q);
     for (int i = tid; i < L::Q_BYTES / 16; i += WORKERS) reinterpret_cast<uint4*>(qf)[i] = make_uint4(0, 0, 0, 0);
     for (int n = tid; n < 2 * NQ; n += WORKERS) fac_sh[n] = 0.f;
+    cp_async_wait_all();
     named_bar_sync(1, WORKERS);
     for (int n = warp; n < g; n += NW) {
       constexpr int E = D / 32;
-      const __nv_bfloat16* qrow = a.q + (static_cast<size_t>(bh) * g + n) * D + lane * E;
+      const __nv_bfloat16* qrow = qraw + n * D + lane * E;
       float y[E];
 #pragma unroll
       for (int i = 0; i < E; ++i) y[i] = __bfloat162float(qrow[i]);
       if (rotated) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) y[i] *= a.signs[lane * E + i];
+        for (int i = 0; i < E; ++i) y[i] *= sign_sh[lane * E + i];
 #pragma unroll
         for (int h = 1; h < E; h <<= 1)
 #pragma unroll
@@ -655,11 +703,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
         const float f = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 24 - k) << 23);
         fac_sh[n] = f;
         if (dup) fac_sh[n + 4] = f;
+        if (a.scores) a.fac[static_cast<size_t>(bh) * NQ + n] = f;
         fac_sh[NQ + n] = sum * (-8.f / kTwo24);
       }
     }
     named_bar_sync(1, WORKERS);
-    float fac[NT][2], x0[NT][2], m_run[NT][2], r_run[NT][2], kq[NT][2], l_run[NT][2], oacc[NT][L::MT][4], ones[NT][4];
+    float fac[NT][2], x0[NT][2], m_run[NT][2], r_run[NT][2], l_run[NT][2], oacc[NT][L::MT][4], ones[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -667,7 +716,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
         fac[j][c] = fac_sh[8 * j + 2 * tq + c];
         x0[j][c] = fac_sh[NQ + 8 * j + 2 * tq + c];
         m_run[j][c] = r_run[j][c] = kKv4Lowest;
-        kq[j][c] = 1.f;
         l_run[j][c] = 0.f;
         ones[j][c] = ones[j][c + 2] = 0.f;
       }
@@ -675,15 +723,20 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
       for (int i = 0; i < L::MT; ++i) oacc[j][i][0] = oacc[j][i][1] = oacc[j][i][2] = oacc[j][i][3] = 0.f;
     }
     const uint2* const qfrag = reinterpret_cast<const uint2*>(qf) + lane;
+    const int len = cur.len;
     // ================= the head's blocks =================================================
-    const int end = min(cur.nblk, cur.blk + left);
-    left -= end - cur.blk;
-    for (int blk = cur.blk; blk < end; ++blk, ++t) {
+    const int end = min(cur.nblk, cur.blk + left), first = cur.blk;
+    left -= end - first;
+    if (left > 0) {  // the query of the head after this one (everybody has read qraw)
+      next_head();
+      fetch_q(cur.bh);
+    }
+    for (int blk = first; blk < end; ++blk, ++t) {
       const int s = t % ST;
       const uint8_t* const st = smem + s * L::STAGE + warp * 32 * L::ROW;
       const int key0 = blk * L::BLOCK + warp * 32;
       ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[s], (t / ST) & 1, abort_sh, 30));
-      if (ok && key0 < cur.len) {
+      if (ok && key0 < len) {
         float x[2][NT][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -734,7 +787,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
         float vs[4];
         const unsigned short* const ksp =
             reinterpret_cast<const unsigned short*>(smem + s * L::STAGE + L::OFF_KS) + warp * 32 + kr;
-        const bool tail = key0 + 32 > cur.len;
+        const bool tail = key0 + 32 > len;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float ks = bf16_bits_to_float(ksp[8 * r]);
@@ -747,14 +800,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
               xa += __shfl_xor_sync(0xffffffffu, xa, 2);
               xb += __shfl_xor_sync(0xffffffffu, xb, 2);
             }
-            xa *= ks * fac[j][0];
-            xb *= ks * fac[j][1];
+            xa *= ks;
+            xb *= ks;
           }
         }
         if (tail) {  // rows behind the last hold anything: neither their codes nor their scales count
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (key0 + 8 * r + kr >= cur.len) {
+            if (key0 + 8 * r + kr >= len) {
               vs[r] = 0.f;
 #pragma unroll
               for (int j = 0; j < NT; ++j) x[r >> 1][j][2 * (r & 1)] = x[r >> 1][j][2 * (r & 1) + 1] = -INFINITY;
@@ -768,7 +821,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
               float* p = a.scores + (static_cast<size_t>(bh) * a.C + key0 + kr) * a.gp + n;
 #pragma unroll
               for (int r = 0; r < 4; ++r)
-                if (!tail || key0 + 8 * r + kr < cur.len) {
+                if (!tail || key0 + 8 * r + kr < len) {
                   if (a.gp == 1) p[8 * r] = x[r >> 1][j][2 * (r & 1)];
                   else *reinterpret_cast<float2*>(p + 8 * r * a.gp) =
                            make_float2(x[r >> 1][j][2 * (r & 1)], x[r >> 1][j][2 * (r & 1) + 1]);
@@ -776,8 +829,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
             }
           }
         }
-        // ---- p = 2^(x - m) and u = p vs 2^(m - R); m and R move only when a p passes 2^8 or a u
-        // passes 2^12, and then both are at most 1 and 2^8 in the second turn ----------------------
+        // ---- p = 2^(x - R) and u = p vs, x = fac times what is stored; R moves only when a u passes
+        // 2^12 (or a p 2^110), and then u is at most 2^8 in the second turn -----------------------------
         float p[2][NT][4], u[2][NT][4];
 #pragma unroll 1
         for (int turn = 0; turn < 2; ++turn) {
@@ -785,25 +838,28 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int r = 0; r < 4; ++r) {
+              float* const pp = &p[r >> 1][j][2 * (r & 1)];
+              float* const uu = &u[r >> 1][j][2 * (r & 1)];
+              const float* const xx = &x[r >> 1][j][2 * (r & 1)];
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const int e = 2 * (r & 1) + c;
-                p[r >> 1][j][e] = ex2_approx(x[r >> 1][j][e] - m_run[j][c]);
-                u[r >> 1][j][e] = p[r >> 1][j][e] * (vs[r] * kq[j][c]);
-                top_p = fmaxf(top_p, p[r >> 1][j][e]);
-                top_u = fmaxf(top_u, u[r >> 1][j][e]);
+              for (int c = 0; c < 2; ++c) {
+                pp[c] = ex2_approx(fmaf(xx[c], fac[j][c], -r_run[j][c]));
+                uu[c] = pp[c] * vs[r];
               }
-          if (turn || !__any_sync(0xffffffffu, top_p > 256.f || top_u > 4096.f)) break;
+              top_p = fmax3(top_p, pp[0], pp[1]);
+              top_u = fmax3(top_u, uu[0], uu[1]);
+            }
+          if (turn || !__any_sync(0xffffffffu, top_p > 1.2980742e33f || top_u > 4096.f)) break;
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            float al[2], be[2];
+            float be[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float mx = -INFINITY, ry = -INFINITY;
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                const float y = x[r >> 1][j][2 * (r & 1) + c];
+                const float y = x[r >> 1][j][2 * (r & 1) + c] * fac[j][c];
                 mx = fmaxf(mx, y);
                 ry = fmaxf(ry, y + __log2f(vs[r]));
               }
@@ -815,12 +871,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
               const float m_new = fmaxf(m_run[j][c], mx);
               // 2^(m - R) stays a normal number
               const float r_new = fminf(fmaxf(fmaxf(r_run[j][c], ry), m_new - 100.f), m_new + 125.f);
-              al[c] = ex2_approx(m_run[j][c] - m_new);
               be[c] = ex2_approx(r_run[j][c] - r_new);
               m_run[j][c] = m_new;
               r_run[j][c] = r_new;
-              kq[j][c] = ex2_approx(m_new - r_new);
-              l_run[j][c] *= al[c];
+              l_run[j][c] *= be[c];
               ones[j][c] *= be[c];
               ones[j][c + 2] *= be[c];
             }
@@ -909,7 +963,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
         for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
         const int n = 8 * j + 2 * tq + c;
         if (grp == 0) {
-          wm[warp * NQ + n] = m_run[j][c];
           wl[warp * NQ + n] = l;
           wr[warp * NQ + n] = r_run[j][c];
         }
@@ -934,13 +987,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
         }
       }
     if (tid < NQ) {
-      float M = kKv4Lowest, R = kKv4Lowest, l = 0.f;
-      for (int w = 0; w < NW; ++w) {
-        M = fmaxf(M, wm[w * NQ + tid]);
-        R = fmaxf(R, wr[w * NQ + tid]);
-      }
-      for (int w = 0; w < NW; ++w) l += wl[w * NQ + tid] * ex2_approx(wm[w * NQ + tid] - M);
-      reinterpret_cast<float4*>(a.part_ml)[slot * NQ + tid] = make_float4(M, l, R, 0.f);
+      float R = kKv4Lowest, l = 0.f;
+      for (int w = 0; w < NW; ++w) R = fmaxf(R, wr[w * NQ + tid]);
+      for (int w = 0; w < NW; ++w) l += wl[w * NQ + tid] * ex2_approx(wr[w * NQ + tid] - R);
+      a.part_rl[slot * NQ + tid] = make_float2(R, l);
     }
     float* const red = reinterpret_cast<float*>(smem + L::OFF_RED);  // [NW][MC][NT][32] float4
     constexpr int RED = L::MC * NT * 128;
@@ -961,7 +1011,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
       }
       named_bar_sync(1, WORKERS);
     }
-    if (left > 0) next_head();
   }
 }
 
@@ -971,7 +1020,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
 template <int D, int NT, int KEYS>
 __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs a) {
   constexpr int NQ = 8 * NT, MT = D / 16, CHUNK = 256 * KEYS;
-  __shared__ float lse2[NQ];
+  __shared__ float lse2[NQ], fac[NQ];
   const int bh = blockIdx.y, g = a.g, tid = threadIdx.x, gp = a.gp;
   const int len = kv4_len(a.lens, bh, a.C);
   const int key0 = blockIdx.x * CHUNK + tid;
@@ -985,7 +1034,7 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
     for (int i = 0; i < KEYS; ++i) {
       const bool in = key0 + 256 * i < len;
       old[i] = in ? a.acc[row + 256 * i] : 0.f;
-      sc[i][0] = sc[i][1] = make_float2(-INFINITY, -INFINITY);
+      sc[i][0] = sc[i][1] = make_float2(0.f, 0.f);
       if (in) {
         const float* p = a.scores + (row + 256 * i) * gp;
         if (gp == 1) sc[i][0].x = p[0];
@@ -1007,17 +1056,18 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
     i0 = static_cast<int>(((b0 + 1) * n_cta - 1) / total);
     i1 = static_cast<int>((b1 * n_cta - 1) / total);
   }
-  const float4* const ml = reinterpret_cast<const float4*>(a.part_ml);
+  const float2* const rl = a.part_rl;
   if (tid < NQ) {
-    float M = kKv4Lowest, L = 0.f;
+    float R = kKv4Lowest, L = 0.f;
     for (int i = i0; i <= i1; ++i) {
-      const float4 p = ml[(static_cast<size_t>(i) + bh) * NQ + tid];
-      const float m_new = fmaxf(M, p.x);
-      L = L * ex2_approx(M - m_new) + p.y * ex2_approx(p.x - m_new);
-      M = m_new;
+      const float2 p = rl[(static_cast<size_t>(i) + bh) * NQ + tid];
+      const float r_new = fmaxf(R, p.x);
+      L = L * ex2_approx(R - r_new) + p.y * ex2_approx(p.x - r_new);
+      R = r_new;
     }
     // heads that are not there weigh nothing
-    lse2[tid] = tid >= g ? INFINITY : len > 0 ? M + log2f(L) : -INFINITY;
+    lse2[tid] = tid >= g ? INFINITY : len > 0 ? R + log2f(L) : -INFINITY;
+    fac[tid] = a.acc && tid < g && len > 0 ? a.fac[static_cast<size_t>(bh) * NQ + tid] : 0.f;
     if (blockIdx.x == 0 && tid < g) a.lse[static_cast<size_t>(bh) * g + tid] = lse2[tid] * 0.69314718055994530942f;
   }
   __syncthreads();
@@ -1029,8 +1079,8 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int p = i0; p <= i1; ++p) {
         const size_t slot = static_cast<size_t>(p) + bh;
-        const float w0 = ex2_approx(ml[slot * NQ + n].z - lse2[n]);
-        const float w1 = ex2_approx(ml[slot * NQ + n + 1].z - lse2[n + 1]);
+        const float w0 = ex2_approx(rl[slot * NQ + n].x - lse2[n]);
+        const float w1 = ex2_approx(rl[slot * NQ + n + 1].x - lse2[n + 1]);
         const float4 v = reinterpret_cast<const float4*>(a.part_o)[slot * MT * NT * 32 + f];
         s.x = fmaf(v.x, w0, s.x);
         s.y = fmaf(v.y, w1, s.y);
@@ -1050,20 +1100,20 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
       }
     }
   if (a.acc) {
+    auto weight = [&](float x, int h) { return h < g ? ex2_approx(fmaf(x, fac[h], -lse2[h])) : 0.f; };
     float w[KEYS];
 #pragma unroll
     for (int i = 0; i < KEYS; ++i) {
-      w[i] = ex2_approx(sc[i][0].x - lse2[0]);
-      if (gp > 1) w[i] += ex2_approx(sc[i][0].y - lse2[1]);
-      if (gp > 2) w[i] += ex2_approx(sc[i][1].x - lse2[2]) + ex2_approx(sc[i][1].y - lse2[3]);
+      w[i] = weight(sc[i][0].x, 0);
+      if (gp > 1) w[i] += weight(sc[i][0].y, 1);
+      if (gp > 2) w[i] += weight(sc[i][1].x, 2) + weight(sc[i][1].y, 3);
     }
     for (int h = 4; h < g; h += 2) {
-      const float l0 = lse2[h], l1 = lse2[h + 1];
 #pragma unroll
       for (int i = 0; i < KEYS; ++i)
         if (key0 + 256 * i < len) {
           const float2 v = *reinterpret_cast<const float2*>(a.scores + (row + 256 * i) * gp + h);
-          w[i] += ex2_approx(v.x - l0) + ex2_approx(v.y - l1);
+          w[i] += weight(v.x, h) + weight(v.y, h + 1);
         }
     }
 #pragma unroll
