@@ -320,7 +320,7 @@ int fa_kv4_read(const void* kc, const void* ks, const void* vc, const void* vs, 
   a.tblocks = (T + rows_per_block - 1) / rows_per_block;
   const long long blocks = static_cast<long long>(B) * H_kv * a.tblocks;
   if (blocks >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(blocks), 2);
+  const unsigned grid = static_cast<unsigned>(blocks);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64) fa::fa_kv4_read_kernel<64><<<grid, 128, 0, s>>>(a);
   else if (d == 128) fa::fa_kv4_read_kernel<128><<<grid, 128, 0, s>>>(a);

@@ -7,10 +7,13 @@
 // Half of the forward's products and all of its exponentials: S^T = K Q^T on tcgen05 with the
 // keys on the tensor-memory lanes, so that one thread holds one key, and the sum over the
 // queries runs along its registers.  128 keys x 128 queries take the tensor core 512 clocks at
-// d = 128 and the exponential unit 1024.  Each column's -lse / scale is one more column of Q against
-// a column of ones of K, in three bf16 pieces: read from shared memory by every thread, four values
-// at a time, the log-sum-exps alone took half of its bandwidth, and the MMAs need the other half
-// (370 us against NEWTIME for 8192 tokens, 32 heads, d = 128).
+// d = 128 and the exponential unit 1024, which bounds it: 8192 tokens, 32 heads, causal, d = 128 take
+// 360 us, of which the exponential unit alone needs 245 (68 % busy; the MMAs alone would need 167).
+// Computing 1 to 3 of 8 exponentials on the FMA pipe instead (a degree-5 polynomial) made it slower
+// each time it was tried (p. e. 1 of 4: 381 us), as did 8 instead of 16 warps with whole score tiles
+// in registers (460 us).
+// Each column's -lse / scale is one more column of Q against a column of ones of K, in three bf16
+// pieces: no thread reads log-sum-exps (369 us when they read them from shared memory).
 //
 // Query rows come in subtiles of 64 rows of one head, and a step takes the next two of them,
 // whatever heads they belong to: with a window of 64 rows the heads that share a key/value head

@@ -52,13 +52,16 @@ struct Kv4AppendArgs {
 // registers: bits 0, 1 and the two that name the lane's quarter are the 16 x 16 matrix H16, one
 // m16n8k16 MMA pair per 4 elements (whose operand is the row as it lies in memory, and whose result
 // has the same layout; half of its rows stay empty: two rows a lane took twice the registers and left
-// too few warps to keep the memory busy, 121 us for the case below); the others are additions between a lane's own pairs.  No shuffles, and a
-// fifth of the instructions of the stages as butterflies: append + read of 262144 rows of d = 128
-// took 122 us with those.
+// too few warps to keep the memory busy, 121 us against 118 for the case below); the others are additions between a lane's own pairs.  No shuffles, and a
+// fifth of the instructions of the stages as butterflies.
+// Append + read of 262144 rows of d = 128 (K and V, 341 MB, 52 us at the copy rate) take 75 us: the
+// butterflies 122 us, this with 16-byte accesses 118, with 32-byte ones 104, without divisions next to
+// a border 87, with eight CTAs per SM (64 registers) 81, K and V of a row read together 75.
 template <int D>
 struct Kv4Rows {
   static constexpr int NE = D / 4, NP = NE / 2, BLOCKS = NE / 4;  // elements, pairs, groups of 4 of a lane and row
   static constexpr int WARPS = 4;                                 // per CTA
+  static constexpr int CTAS = D == 256 ? 4 : 8;                   // per SM: 64 (128) registers a thread
   static constexpr int RPL = 1, ROWS = 8 * RPL;                   // rows of a lane, of a warp
 };
 
@@ -112,19 +115,14 @@ __device__ __forceinline__ void kv4_sign_masks(const float* signs, uint32_t* mas
 // fp32 number.  (The quotient has to be the rounded one: y / s is often an exact tie of two codes, as
 // s and an unrotated y have 8 bits.)
 template <int D>
-__global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS) fa_kv4_append_kernel(const Kv4AppendArgs a) {
+__global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_kv4_append_kernel(const Kv4AppendArgs a) {
   using R = Kv4Rows<D>;
   __shared__ __align__(16) uint32_t masks[D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane >> 2, tq = lane & 3;
   const int bh = blockIdx.x / a.tblocks;
   const int t0 = (blockIdx.x % a.tblocks) * (R::ROWS * R::WARPS) + warp * R::ROWS;
   const bool is_v = blockIdx.y == 1, rotate = !is_v && a.signs;
-  if (rotate) {
-    kv4_sign_masks<D>(a.signs, masks);
-    __syncthreads();
-  }
   const int n_new = a.n_new ? min(a.n_new[bh], a.T) : a.T;
-  if (t0 >= n_new) return;
   int src[R::RPL];
   long long dst[R::RPL];
   bool live[R::RPL];
@@ -146,6 +144,17 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS) fa_kv4_append_kernel(c
         for (int i = 0; i < 8; ++i) w[r][8 * u + i] = 0u;
     }
   }
+  const bool notes = !is_v && tq == 0;  // the lane that writes the row's weight and position
+  float weight[R::RPL];
+#pragma unroll
+  for (int r = 0; r < R::RPL; ++r)
+    weight[r] = notes && live[r] && a.acc && a.w ? a.w[static_cast<size_t>(bh) * a.ldw + src[r]] : 0.f;
+  const int base = notes && a.base ? a.base[bh / a.Hkv] : 0;
+  if (rotate) {  // (the rows are on their way)
+    kv4_sign_masks<D>(a.signs, masks);
+    __syncthreads();
+  }
+  if (t0 >= n_new) return;
   float2 z[R::RPL][R::NP];
   if (rotate) {
 #pragma unroll
@@ -227,8 +236,8 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS) fa_kv4_append_kernel(c
     if (tq == 0) {
       (is_v ? a.vs : a.ks)[row] = sb;
       if (!is_v) {
-        if (a.acc) a.acc[row] = a.w ? a.w[static_cast<size_t>(bh) * a.ldw + src[r]] : 0.f;
-        if (a.pos) a.pos[row] = (a.base ? a.base[bh / a.Hkv] : 0) + src[r];
+        if (a.acc) a.acc[row] = weight[r];
+        if (a.pos) a.pos[row] = base + src[r];
       }
     }
   }
@@ -256,43 +265,70 @@ struct Kv4ReadArgs {
 // even ones and n 2^-20 the odd ones, against +-2^14 and +-2^10; H of the eights is 8 d in element 0
 // and nothing elsewhere.
 template <int D>
-__global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS) fa_kv4_read_kernel(const Kv4ReadArgs a) {
+__global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_kv4_read_kernel(const Kv4ReadArgs a) {
   using R = Kv4Rows<D>;
   __shared__ __align__(16) uint32_t masks[D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane >> 2, tq = lane & 3;
   const int bh = blockIdx.x / a.tblocks;
-  const int t0 = (blockIdx.x % a.tblocks) * (R::ROWS * R::WARPS) + warp * R::ROWS;
-  const bool is_v = blockIdx.y == 1, rotate = !is_v && a.signs;
-  if (rotate) {
+  const int t0 = (blockIdx.x % a.tblocks) * (R::ROWS * R::WARPS) + warp * R::ROWS, t = t0 + grp;
+  const int len = a.lens ? min(a.lens[bh], a.C) : a.C;
+  long long at = -1;
+  if (t < a.T) at = a.slots ? a.slots[static_cast<long long>(bh) * a.T + t] : static_cast<long long>(a.first) + t;
+  const bool live = at >= 0 && at < len;
+  const size_t row = static_cast<size_t>(bh) * a.C + (live ? at : 0);
+  // the key's and the value's codes and scales, all on their way together
+  uint32_t w[2][R::NE / 8];
+  float s[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const uint8_t* codes = (x ? a.vc : a.kc) + row * (D / 2) + tq * 8;
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u) {
+      const uint2 v = *reinterpret_cast<const uint2*>(codes + 32 * u);
+      w[x][2 * u] = v.x, w[x][2 * u + 1] = v.y;
+    }
+    s[x] = __bfloat162float((x ? a.vs : a.ks)[row]);
+    if (!live) {  // zeros, whatever the row holds
+      s[x] = 0.f;
+#pragma unroll
+      for (int i = 0; i < R::NE / 8; ++i) w[x][i] = 0x88888888u;
+    }
+  }
+  if (a.signs) {
     kv4_sign_masks<D>(a.signs, masks);
     __syncthreads();
   }
   if (t0 >= a.T) return;
-  const int len = a.lens ? min(a.lens[bh], a.C) : a.C;
-  uint32_t w[R::RPL][R::NE / 8];
-  float s[R::RPL];
+  uint32_t x[R::NP];  // the row's pairs of bf16
+  auto store = [&](__nv_bfloat16* to) {
+    if (t >= a.T) return;
+    __nv_bfloat16* out = to + (static_cast<long long>(bh) * a.T + t) * D + tq * 16;
 #pragma unroll
-  for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
-    const int t = t0 + grp + 8 * r;
-    long long at = -1;
-    if (t < a.T) at = a.slots ? a.slots[static_cast<long long>(bh) * a.T + t] : static_cast<long long>(a.first) + t;
-    const bool live = at >= 0 && at < len;
-    const size_t row = static_cast<size_t>(bh) * a.C + (live ? at : 0);
-    const uint8_t* codes = (is_v ? a.vc : a.kc) + row * (D / 2) + tq * 8;
+    for (int u = 0; u < D / 64; ++u) st_global_32(out + 64 * u, &x[8 * u]);
+  };
+  auto plain = [&](const uint32_t (&w)[R::NE / 8], float s) {
+    // codes as bf16, (128 + n) - 136, times the scale: a product of 4 and 8 bits, rounded once
+    const uint32_t s2 = pack_bf16x2(s, s);
 #pragma unroll
-    for (int u = 0; u < D / 64; ++u) {
-      const uint2 v = *reinterpret_cast<const uint2*>(codes + 32 * u);
-      w[r][2 * u] = v.x, w[r][2 * u + 1] = v.y;
+    for (int i = 0; i < R::NE / 8; ++i) {
+      uint32_t v[4];  // elements (0, 4), (1, 5), (2, 6), (3, 7)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t n = ((w[i] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(v[e]) : "r"(n), "r"(0xC308C308u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v[e]) : "r"(v[e]), "r"(s2));
+      }
+      x[4 * i] = __byte_perm(v[0], v[1], 0x5410);
+      x[4 * i + 1] = __byte_perm(v[2], v[3], 0x5410);
+      x[4 * i + 2] = __byte_perm(v[0], v[1], 0x7632);
+      x[4 * i + 3] = __byte_perm(v[2], v[3], 0x7632);
     }
-    s[r] = __bfloat162float((is_v ? a.vs : a.ks)[row]);
-    if (!live) {  // zeros, whatever the row holds
-      s[r] = 0.f;
-#pragma unroll
-      for (int i = 0; i < R::NE / 8; ++i) w[r][i] = 0x88888888u;
-    }
-  }
-  uint32_t x[R::RPL][R::NP];  // the rows' pairs of bf16
-  if (rotate) {
+  };
+  plain(w[1], s[1]);
+  store(a.v);
+  if (!a.signs) {
+    plain(w[0], s[0]);
+  } else {
     float2 z[R::RPL][R::NP];
     uint32_t b[2][2];
 #pragma unroll
@@ -305,64 +341,32 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS) fa_kv4_read_kernel(con
       }
 #pragma unroll
     for (int g = 0; g < R::BLOCKS; ++g) {
-      uint32_t p[R::RPL][2];  // bytes 2 g, 2 g + 1 of the lane's codes, a byte in each half
+      uint32_t p[2];  // bytes 2 g, 2 g + 1 of the lane's codes, a byte in each half
 #pragma unroll
-      for (int r = 0; r < Kv4Rows<D>::RPL; ++r)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          p[r][h] = __byte_perm(w[r][g >> 1], 0u, (g & 1) ? (h ? 0x4343 : 0x4242) : (h ? 0x4141 : 0x4040)) & 0x00f0000fu;
+      for (int h = 0; h < 2; ++h)
+        p[h] = __byte_perm(w[0][g >> 1], 0u, (g & 1) ? (h ? 0x4343 : 0x4242) : (h ? 0x4141 : 0x4040)) & 0x00f0000fu;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
         float c[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_16816_f16(c, p[0][0], 0u, p[0][1], 0u, b[nt][0], b[nt][1]);
+        mma_16816_f16(c, p[0], 0u, p[1], 0u, b[nt][0], b[nt][1]);
         z[0][2 * g + nt] = make_float2(c[0], c[1]);
       }
     }
     kv4_hadamard_groups<D>(z);
+    if (tq == 0) z[0][0].x -= 8.f * D / 1024.f;
+    float f = s[0] * (1024.f / D);
+    if (s[0] > 1e30f) {  // the product of the factors could pass fp32's range
+      f = s[0];
 #pragma unroll
-    for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
-      if (tq == 0) z[r][0].x -= 8.f * D / 1024.f;
-      float f = s[r] * (1024.f / D);
-      if (s[r] > 1e30f) {  // the product of the factors could pass fp32's range
-        f = s[r];
-#pragma unroll
-        for (int i = 0; i < R::NP; ++i) z[r][i] = fmul2(z[r][i], make_float2(1024.f / D, 1024.f / D));
-      }
-#pragma unroll
-      for (int i = 0; i < R::NP; ++i) {
-        const float2 v = fmul2(z[r][i], make_float2(f, f));
-        x[r][i] = pack_bf16x2(v.x, v.y) ^ masks[32 * (i >> 3) + tq * 8 + (i & 7)];
-      }
+      for (int i = 0; i < R::NP; ++i) z[0][i] = fmul2(z[0][i], make_float2(1024.f / D, 1024.f / D));
     }
-  } else {
-    // codes as bf16, (128 + n) - 136, times the scale: a product of 4 and 8 bits, rounded once
 #pragma unroll
-    for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
-      const uint32_t s2 = pack_bf16x2(s[r], s[r]);
-#pragma unroll
-      for (int i = 0; i < R::NE / 8; ++i) {
-        uint32_t v[4];  // elements (0, 4), (1, 5), (2, 6), (3, 7)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t n = ((w[r][i] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
-          asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(v[e]) : "r"(n), "r"(0xC308C308u));
-          asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v[e]) : "r"(v[e]), "r"(s2));
-        }
-        x[r][4 * i] = __byte_perm(v[0], v[1], 0x5410);
-        x[r][4 * i + 1] = __byte_perm(v[2], v[3], 0x5410);
-        x[r][4 * i + 2] = __byte_perm(v[0], v[1], 0x7632);
-        x[r][4 * i + 3] = __byte_perm(v[2], v[3], 0x7632);
-      }
+    for (int i = 0; i < R::NP; ++i) {
+      const float2 v = fmul2(z[0][i], make_float2(f, f));
+      x[i] = pack_bf16x2(v.x, v.y) ^ masks[32 * (i >> 3) + tq * 8 + (i & 7)];
     }
   }
-#pragma unroll
-  for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
-    const int t = t0 + grp + 8 * r;
-    if (t >= a.T) continue;
-    __nv_bfloat16* out = (is_v ? a.v : a.k) + (static_cast<long long>(bh) * a.T + t) * D + tq * 16;
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u) st_global_32(out + 64 * u, &x[r][8 * u]);
-  }
+  store(a.k);
 }
 
 // ---------------------------------------------------------------------------
