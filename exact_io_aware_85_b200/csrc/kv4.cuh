@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
 //     the nibbles n = c + 8, and w & 0xf000f0 is n 2^-20, exact in the MMA; one shift by 8 serves
 //     the other half of the word.  The factor 16 goes into q (for K) or into the result (for V).
 //     The 8 leaves K's products through the accumulator's start, -8 sum(q), and V's through one
-//     more MMA whose codes are all 8: it gathers 8 sum(P), which is taken off at the end.
+//     more MMA whose codes are all 8: it gathers 8 sum(P), which is taken off at the end (an
+//     absolute error of some 2^-20 sum(p vs), below a bf16 output's rounding unless the weighty
+//     rows' codes are all zero in a column).
 //     (fp16 1024 + n and an addition instead: 594 instead of about 400 instructions per 32 keys
 //     of d = 128, and the same in bf16 for V.)
 //   * q in fp16, scaled by a power of two per head so that its largest element is near 2^14: a
@@ -398,7 +400,8 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
 //   * P times the row's scale, u = p vs, meets V's codes in fp16 too (11 bits, so its rounding
 //     stays below that of the bf16 output).  Its range: p = 2^(x - R) with R a running maximum of
 //     x + log2 vs instead of x, so that u stays near one and what flushes is 2^-24 of the largest;
-//     the softmax's sum is held relative to the same R.
+//     the softmax's sum is held relative to the same R, which stays within -92 and +125 of the
+//     maximum of x: rows whose values are zero or tiny keep their share of the sum.
 //   * Work is one list of blocks over all heads' lengths, cut into equal parts, one per CTA:
 //     ragged batches fill the GPU evenly.
 struct Kv4DecodeArgs {
@@ -425,6 +428,13 @@ struct Kv4DecodeArgs {
 __device__ __forceinline__ int kv4_len(const int* lens, int bh, int C) { return max(0, min(lens[bh], C)); }
 
 constexpr float kKv4Lowest = -3.0e38f;  // the running maximum before the first key
+
+// l 2^x in two steps: a sum of p may hold numbers near 2^97 (rows whose values are zero or tiny
+// leave R far below their scores), so that 2^x alone can be 0 where the product counts
+__device__ __forceinline__ float kv4_rescale(float l, float x) {
+  const float h = ex2_approx(0.5f * x);
+  return l * h * h;
+}
 
 // Working warps per CTA; one more loads.  As many as the registers of the output and the codes
 // leave room for: 128, 168 or 255 a thread.
@@ -834,7 +844,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
           }
         }
         // ---- p = 2^(x - R) and u = p vs, x = fac times what is stored; R moves only when a u passes
-        // 2^12 (or a p 2^110), and then u is at most 2^8 in the second turn -----------------------------
+        // 2^12 (or a p 2^97), and then u is at most 2^8 in the second turn -----------------------------
         float p[2][NT][4], u[2][NT][4];
 #pragma unroll 1
         for (int turn = 0; turn < 2; ++turn) {
@@ -854,7 +864,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
               top_p = fmax3(top_p, pp[0], pp[1]);
               top_u = fmax3(top_u, uu[0], uu[1]);
             }
-          if (turn || !__any_sync(0xffffffffu, top_p > 1.2980742e33f || top_u > 4096.f)) break;
+          if (turn || !__any_sync(0xffffffffu, top_p > 1.5845633e29f || top_u > 4096.f)) break;
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             float be[2];
@@ -873,12 +883,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
                 ry = fmaxf(ry, __shfl_xor_sync(0xffffffffu, ry, off));
               }
               const float m_new = fmaxf(m_run[j][c], mx);
-              // 2^(m - R) stays a normal number
-              const float r_new = fminf(fmaxf(fmaxf(r_run[j][c], ry), m_new - 100.f), m_new + 125.f);
+              // 2^(m - R) stays a normal number, and the sum of 2^30 p below 2^128
+              const float r_new = fminf(fmaxf(fmaxf(r_run[j][c], ry), m_new - 92.f), m_new + 125.f);
               be[c] = ex2_approx(r_run[j][c] - r_new);
+              l_run[j][c] = kv4_rescale(l_run[j][c], r_run[j][c] - r_new);
               m_run[j][c] = m_new;
               r_run[j][c] = r_new;
-              l_run[j][c] *= be[c];
               ones[j][c] *= be[c];
               ones[j][c + 2] *= be[c];
             }
@@ -993,7 +1003,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
     if (tid < NQ) {
       float R = kKv4Lowest, l = 0.f;
       for (int w = 0; w < NW; ++w) R = fmaxf(R, wr[w * NQ + tid]);
-      for (int w = 0; w < NW; ++w) l += wl[w * NQ + tid] * ex2_approx(wr[w * NQ + tid] - R);
+      for (int w = 0; w < NW; ++w) l += kv4_rescale(wl[w * NQ + tid], wr[w * NQ + tid] - R);
       a.part_rl[slot * NQ + tid] = make_float2(R, l);
     }
     float* const red = reinterpret_cast<float*>(smem + L::OFF_RED);  // [NW][MC][NT][32] float4
@@ -1066,7 +1076,7 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
     for (int i = i0; i <= i1; ++i) {
       const float2 p = rl[(static_cast<size_t>(i) + bh) * NQ + tid];
       const float r_new = fmaxf(R, p.x);
-      L = L * ex2_approx(R - r_new) + p.y * ex2_approx(p.x - r_new);
+      L = kv4_rescale(L, R - r_new) + kv4_rescale(p.y, p.x - r_new);
       R = r_new;
     }
     // heads that are not there weigh nothing

@@ -382,3 +382,116 @@ def test_binding_refusals_on_a_gpu():
             fa.fa_decode_kv4(**dict(good, **{name: bad}))
     with pytest.raises(fa.FAError):
         fa.fa_decode_kv4(**dict(good, acc=torch.zeros((B, Hkv, C), device=DEV)))  # the workspace is too small with acc
+
+
+@pytest.mark.parametrize("power", [-100, -60, 60, 100])
+def test_decode_queries_of_any_size(power):
+    """Queries far from one, with a softmax scale that brings the scores back."""
+    from exact_io_aware_85_b200 import fa
+    B, H, Hkv, C, d = 1, 4, 2, 256, 64
+    q = (_randn(1, B, H, d).float() * 2.0 ** power).to(torch.bfloat16)
+    k, v = _randn(2, B, Hkv, C, d), _randn(3, B, Hkv, C, d)
+    for signs in (None, _signs(d, 4)):
+        cache = _cache(B, Hkv, C, d)
+        fa.fa_kv4_append(k, v, *cache, signs=signs)
+        lens = torch.full((B, Hkv), C, dtype=torch.int32, device=DEV)
+        o, lse = torch.empty((B, H, d), dtype=torch.bfloat16, device=DEV), torch.empty((B, H), device=DEV)
+        ws = torch.empty(fa.fa_decode_kv4_workspace_bytes(B, H, Hkv, C, d, False), dtype=torch.uint8, device=DEV)
+        scale = 2.0 ** -power / 8
+        fa.fa_decode_kv4(q, *cache, lens, o, lse, scale, ws, signs=signs)
+        cs = None if signs is None else signs.cpu()
+        kr, vr = R.values(cache[0].cpu(), cache[1].cpu().float(), cs), R.values(cache[2].cpu(), cache[3].cpu().float())
+        ro, rl, _, pv, terms = R.decode(q.cpu().double(), kr, vr, lens.cpu(), scale)
+        # in the rotated basis the terms of a score can be larger: a row's terms there are at most |q| |k| in norm
+        norms = scale * q.cpu().double().norm(dim=-1) * kr.norm(dim=-1).amax(-1).repeat_interleave(H // Hkv, 1)
+        t_o, t_lse, _ = _bounds(d, C, torch.maximum(terms, norms), rl, pv, ro)
+        assert ((o.cpu().double() - ro).abs() <= t_o).all()
+        assert ((lse.cpu().double() - rl).abs() <= t_lse).all()
+
+
+def test_a_cache_past_four_gigabytes():
+    """Row offsets past 2^32 bytes, and scores past 2^31 bytes: the second head's last rows carry everything."""
+    from exact_io_aware_85_b200 import fa
+    B, H, Hkv, C, d = 1, 8, 2, 1 << 25, 128
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    kc, vc = (torch.full((B, Hkv, C, d // 2), 0x88, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros((B, Hkv, C), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    cache = (kc, ks, vc, vs)
+    n = 5
+    k, v, q = _randn(1, B, Hkv, n, d), _randn(2, B, Hkv, n, d), _randn(3, B, H, d)
+    k = (k.float() * 20).to(torch.bfloat16)
+    start = torch.tensor([[0, C - n]], dtype=torch.int32, device=DEV)
+    acc, pos = torch.zeros((B, Hkv, C), device=DEV), torch.zeros((B, Hkv, C), dtype=torch.int32, device=DEV)
+    fa.fa_kv4_append(k, v, *cache, start=start, acc=acc, pos=pos)
+    assert pos[0, 1, C - n:].tolist() == list(range(n)) and pos[0, 0, :n].tolist() == list(range(n))
+    lens = torch.tensor([[n, C]], dtype=torch.int32, device=DEV)
+    o, lse = torch.empty((B, H, d), dtype=torch.bfloat16, device=DEV), torch.empty((B, H), device=DEV)
+    ws = torch.empty(fa.fa_decode_kv4_workspace_bytes(B, H, Hkv, C, d, True), dtype=torch.uint8, device=DEV)
+    scale = 1 / math.sqrt(d)
+    fa.fa_decode_kv4(q, *cache, lens, o, lse, scale, ws, acc=acc)
+    torch.cuda.synchronize()
+    assert fa.fa_check_status() == fa.FA_OK
+    for hk, lo in ((0, 0), (1, C - n)):
+        kr, vr = (R.values(cache[a][:, hk:hk + 1, lo:lo + n].cpu(), cache[a + 1][:, hk:hk + 1, lo:lo + n].cpu().float())
+                  for a in (0, 2))
+        qh = q.cpu().double()[:, 4 * hk:4 * hk + 4]
+        s = scale * qh[0] @ kr[0, 0].T                      # the other C - n rows score zero, with values of zero
+        zeros = C - n if hk else 0
+        l = torch.exp(s).sum(-1) + zeros
+        p = torch.exp(s) / l[:, None]
+        want = p @ vr[0, 0]
+        # V's codes c enter the products as c + 8 and the eights leave by a subtraction: sum u (c + 8) and 8 sum u,
+        # u = p vs, are sums of numbers of at most 15 u, each addition rounded to 2^-24 of the sum so far, 15 sum u.
+        # A warp adds a block of 32 of every 480 keys of its CTA's part in two additions, and 20 more join the parts:
+        # adds * 2^-24 * (15 + 8) sum u, which counts where the weighty rows' codes are zero (want is near zero there)
+        adds = 2 * (C // (148 * 480) + 1) + 20
+        eights = adds * 2.0 ** -24 * 23 * (p @ cache[3][0, hk, lo:lo + n].cpu().double())[:, None]
+        assert ((o[0, 4 * hk:4 * hk + 4].cpu().double() - want).abs()
+                <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -10) * (p @ vr[0, 0].abs()) + eights).all()
+        # sums of 2^25 equal terms in chains of 2^25 / (148 * 480): 2^9 roundings of 2^-24
+        assert ((lse[0, 4 * hk:4 * hk + 4].cpu().double() - torch.log(l)).abs() <= 2.0 ** -12).all()
+        got = acc[0, hk, lo:lo + n].cpu().double()
+        assert ((got - p.sum(0)).abs() <= 2.0 ** -11 * p.sum(0) + 1e-7).all()
+    slots = torch.empty((B, Hkv, 3), dtype=torch.int32, device=DEV)
+    seen = torch.full((B,), C, dtype=torch.int32, device=DEV)
+    acc.fill_(1.0)
+    acc[0, 1, C - 2] = 0.5
+    acc[0, 1, C - 9] = 0.25
+    pos.fill_(7)
+    fa.fa_evict_slots(acc, pos, lens, seen, slots, C, 1, 1)
+    assert slots[0, 1].tolist() == [C - 9, C - 2, C - 1] and slots[0, 0].tolist() == [n, n + 1, n + 2]
+    ko, vo = torch.empty((B, Hkv, 3, d), dtype=torch.bfloat16, device=DEV), torch.empty((B, Hkv, 3, d), dtype=torch.bfloat16, device=DEV)
+    fa.fa_kv4_read(*cache, ko, vo, slots=slots)
+    want = R.values(cache[2][0, 1, C - 2:].cpu(), cache[3][0, 1, C - 2:].cpu().float())
+    assert torch.equal(vo[0, 1, 1:].cpu(), want.to(torch.bfloat16))
+
+
+def test_decode_rows_without_values_keep_their_weight():
+    """Rows whose V is zero, or tiny, beside rows whose V is not: they take their share of the softmax all the same,
+    in every order (the sum is held relative to a reference that follows score and value scale)."""
+    from exact_io_aware_85_b200 import fa
+    B, H, Hkv, C, d = 1, 4, 1, 2048, 64
+    g = torch.Generator().manual_seed(11)
+    q, k = torch.randn((B, H, d), generator=g), torch.randn((B, Hkv, C, d), generator=g)
+    base = torch.randn((B, Hkv, C, d), generator=g)
+    rows = torch.arange(C)[:, None]
+    for which, small in (("early", rows < C - 3), ("late", rows >= 3), ("most", rows % 700 != 5), ("all", rows >= 0)):
+        for factor in (0.0, 1e-24, 1e-12):
+            v = torch.where(small, base * factor, base)
+            qq, kk, vv = (t.to(torch.bfloat16).to(DEV) for t in (q * 2, k, v))
+            cache = _cache(B, Hkv, C, d)
+            fa.fa_kv4_append(kk, vv, *cache)
+            lens = torch.full((B, Hkv), C, dtype=torch.int32, device=DEV)
+            o, lse, acc = torch.empty((B, H, d), dtype=torch.bfloat16, device=DEV), torch.empty((B, H), device=DEV), torch.zeros((B, Hkv, C), device=DEV)
+            ws = torch.empty(fa.fa_decode_kv4_workspace_bytes(B, H, Hkv, C, d, True), dtype=torch.uint8, device=DEV)
+            fa.fa_decode_kv4(qq, *cache, lens, o, lse, 0.5, ws, acc=acc)
+            kr, vr = (R.values(cache[a].cpu(), cache[a + 1].cpu().float()) for a in (0, 2))
+            ro, rl, rw, pv, terms = R.decode(qq.cpu().double(), kr, vr, lens.cpu(), 0.5)
+            _, t_lse, t_w = _bounds(d, C, terms, rl, pv, ro)
+            assert ((lse.cpu().double() - rl).abs() <= t_lse).all(), (which, factor)
+            assert ((acc.cpu().double() - rw).abs() <= t_w.amax() * rw + 2.0 ** -22 * (1 + rw)).all(), (which, factor)
+            # O's own rounding to bf16 is 2^-8 of it; P's to fp16 (2^-11, or 2^-25 2^8 absolute beside the largest u)
+            # and the offset's cancellation (2^-20 sum p vs, at most 8 times the largest |o|) stay below another 2^-8
+            top = ro.abs().amax(-1, keepdim=True) + pv.amax(-1, keepdim=True)
+            assert ((o.cpu().double() - ro).abs() <= 2.0 ** -7 * top).all(), (which, factor)
