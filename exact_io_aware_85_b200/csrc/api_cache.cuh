@@ -173,6 +173,7 @@ int fa_key_weights(const void* q, const void* k, const float* lse, float* w, con
   if (B < 1 || H < 1 || H_kv < 1 || N < 1 || H % H_kv != 0 || window < 1 || ldw < N) return FA_ERR_INVALID_ARG;
   if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (!head_dim_ok(d) || !sizes_fit(B, H, N, d)) return FA_ERR_UNSUPPORTED;
+  if (scale < 8.271806e-25f) return FA_ERR_UNSUPPORTED;  // 2^-80: lse / scale has to be a number
   if (!aligned16(q) || !aligned16(k) || !aligned4(lse) || !aligned4(w) || !aligned4(n_rows) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return FA_ERR_ALIGNMENT;

@@ -128,7 +128,7 @@ def test_key_weights(lib):
     for n in "B H Hkv N window".split():
         assert go(**{n: 0}) == INVALID, n
     assert go(H=3) == INVALID and go(ldw=49) == INVALID and go(scale=0.0) == INVALID
-    assert go(d=96) == UNSUPPORTED
+    assert go(d=96) == UNSUPPORTED and go(scale=1e-30) == UNSUPPORTED
     assert lib.fa_key_weights_workspace_bytes(1, 4, 2, 50, 64, 8) > 0
     assert go(nws=0) == INVALID
     assert lib.fa_key_weights_workspace_bytes(1, 3, 2, 50, 64, 8) == 0

@@ -96,3 +96,47 @@ def test_rows_that_hold_anything_outside_the_window():
         fa.fa_key_weights(a.to(DEV), b.to(DEV), c.to(DEV), w, True, scale, ws, window=window, n_rows=n_rows.to(DEV))
         out.append(w)
     assert torch.equal(*out)
+
+
+def test_the_same_bits_again_and_from_a_graph():
+    from exact_io_aware_85_b200 import fa
+    B, H, Hkv, N, d = 2, 8, 2, 1111, 128
+    n_rows = torch.tensor([1111, 640], dtype=torch.int32, device=DEV)
+    q, k, lse, scale, _ = _inputs(B, H, Hkv, N, d, 5, True, n_rows.cpu())
+    q, k, lse = q.to(DEV), k.to(DEV), lse.to(DEV)
+    ws = torch.empty(fa.fa_key_weights_workspace_bytes(B, H, Hkv, N, d, 500), dtype=torch.uint8, device=DEV)
+    w = [torch.empty((B, Hkv, N), device=DEV) for _ in range(4)]
+    fa.fa_key_weights(q, k, lse, w[0], True, scale, ws, window=500, n_rows=n_rows)
+    ws.fill_(255)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    fa.fa_key_weights(q, k, lse, w[1], True, scale, ws, window=500, n_rows=n_rows, stream=side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.fa_key_weights(q, k, lse, w[2], True, scale, ws, window=500, n_rows=n_rows)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(w[0], w[1]) and torch.equal(w[0], w[2])
+    n_rows.fill_(300)  # the graph follows the lengths
+    graph.replay()
+    fa.fa_key_weights(q, k, lse, w[3], True, scale, ws, window=500, n_rows=n_rows)
+    torch.cuda.synchronize()
+    assert torch.equal(w[2], w[3]) and (w[3][:, :, 300:] == 0).all()
+    assert fa.fa_check_status() == fa.FA_OK
+
+
+def test_log_sum_exps_that_are_not_finite():
+    """A row with lse = +infinity gives nothing; one with NaN makes the weight of every key it sees NaN."""
+    from exact_io_aware_85_b200 import fa
+    B, H, Hkv, N, d = 1, 2, 2, 300, 64
+    q, k, lse, scale, _ = _inputs(B, H, Hkv, N, d, 6, True)
+    lse[0, 0, 200] = float("inf")
+    lse[0, 1, 200] = float("nan")
+    ws = torch.empty(fa.fa_key_weights_workspace_bytes(B, H, Hkv, N, d, N), dtype=torch.uint8, device=DEV)
+    w = torch.empty((B, Hkv, N), device=DEV)
+    fa.fa_key_weights(q.to(DEV), k.to(DEV), lse.to(DEV), w, True, scale, ws)
+    want = R.key_weights(q.double(), k.double(), lse.double(), True, scale, N)
+    assert torch.isnan(w[0, 1, :201]).all() and torch.isfinite(w[0, 1, 201:]).all()
+    # relative 2^-16 covers what the finite rows' arithmetic may be off (see the tolerance above)
+    assert ((w[0, 0].cpu().double() - want[0, 0]).abs() <= 2.0 ** -16 * want[0, 0]).all()
