@@ -126,14 +126,7 @@ int launch_key_weights(const void* q, const void* k, int B, int H, int Hkv, int 
                       dim3(256), s, a);
 }
 
-// Eviction: CTAs per head (a cluster of up to sixteen), while the grid stays within the SMs.
-template <bool SLOTS, int ITEMS>
-cudaError_t launch_evict_items(const cudaLaunchConfig_t& cfg, const fa::EvictArgs& a) {
-  const cudaError_t e = cudaFuncSetAttribute(fa::fa_evict_kernel<SLOTS, ITEMS>,
-                                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, fa::fa_evict_kernel<SLOTS, ITEMS>, a) : e;
-}
-
+// Eviction: CTAs per head (a cluster of up to eight), while the grid stays within the SMs.
 template <bool SLOTS>
 int launch_evict(fa::EvictArgs a, int heads, int rows, cudaStream_t s) {
   int S = 1;
@@ -150,9 +143,9 @@ int launch_evict(fa::EvictArgs a, int heads, int rows, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const int per = (rows + S - 1) / S;
-  const cudaError_t e = per <= 4096   ? launch_evict_items<SLOTS, 4>(cfg, a)
-                        : per <= 8192 ? launch_evict_items<SLOTS, 8>(cfg, a)
-                                      : launch_evict_items<SLOTS, 16>(cfg, a);
+  const cudaError_t e = per <= 4096   ? cudaLaunchKernelEx(&cfg, fa::fa_evict_kernel<SLOTS, 4>, a)
+                        : per <= 8192 ? cudaLaunchKernelEx(&cfg, fa::fa_evict_kernel<SLOTS, 8>, a)
+                                      : cudaLaunchKernelEx(&cfg, fa::fa_evict_kernel<SLOTS, 16>, a);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 

@@ -16,7 +16,7 @@
 
 namespace {
 
-void* g_fn[8];  // addresses of the library's entry points, in the order of `bind`
+void* g_fn[6];  // addresses of the library's entry points, in the order of `bind`
 enum { kKeyWeights, kEvictKeep, kEvictSlots, kAppend, kRead, kDecode };
 
 constexpr auto BF16 = at::ScalarType::BFloat16;
@@ -68,6 +68,11 @@ struct Call {
     if (overflow || v > INT32_MAX || v < INT32_MIN) bad = true;
     return static_cast<int>(v);
   }
+  int truth(int i) {
+    const int v = PyObject_IsTrue(args[i]);
+    if (v < 0) PyErr_Clear(), bad = true;
+    return v > 0;
+  }
   // None: the current stream of the current device
   void* stream(int i) {
     if (args[i] == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
@@ -105,7 +110,7 @@ PyObject* key_weights(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int64_t B = q->size(0), H = q->size(1), N = q->size(2), d = q->size(3), Hkv = k->size(1), ldw = w->size(2);
     void* p[6] = {c.get(0, BF16, {B, H, N, d}, true), c.get(1, BF16, {B, Hkv, N, d}, true), c.get(2, F32, {B, H, N}, true),
                   c.get(3, F32, {B, Hkv, ldw}, true), c.get(4, I32, {B}, false), c.get(5, U8, {ws->size(0)}, true)};
-    const int causal = PyObject_IsTrue(c.args[6]) != 0;
+    const int causal = c.truth(6);
     const int window = c.args[7] == Py_None ? static_cast<int>(N) : c.integer(7);
     const float scale = static_cast<float>(c.number(8));
     if (c.bad || !fits_int({B, H, Hkv, N, ldw, d})) return -1;

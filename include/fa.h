@@ -240,7 +240,8 @@ int fa_fwd_fp8_gqa(const void* q8, const void* k8, const void* v8, const float* 
  * n_rows: int32 [B] or NULL: tokens of each sequence (N); rows behind them neither give nor
  * get weight (their w is 0).  The window is the last `window` rows of each sequence (window >= N:
  * all of them).  w: fp32 [B,H_kv,ldw], ldw >= N; columns 0 .. N-1 are overwritten.  scale >= 2^-80.
- * workspace: >= fa_key_weights_workspace_bytes(). */
+ * workspace: >= fa_key_weights_workspace_bytes(), one for each of the calls that may run at the
+ * same time. */
 size_t fa_key_weights_workspace_bytes(int B, int H, int H_kv, int N, int d, int window);
 int fa_key_weights(const void* q, const void* k, const float* lse, float* w, const int* n_rows, int B, int H, int H_kv,
                    int N, int ldw, int d, int causal, int window, float scale, void* workspace, size_t workspace_bytes,
@@ -286,10 +287,12 @@ int fa_kv4_read(const void* kc, const void* ks, const void* vc, const void* vs, 
  * query head h reads key/value head h / (H / H_kv), at most 16 query heads share one.  signs:
  * as given to fa_kv4_append (the query is rotated inside).  A head with no rows gives o = 0 and
  * lse = -inf.  acc (or NULL): acc[b,hk,j] += the sum over the query heads that share hk of
- * their softmax weight of row j.  A query (rotated, where signs is given) of magnitudes below 2^110
- * is taken exactly (22 bits where rotated).  Scales of V from 2^-80 to 2^90 cost no accuracy (below, o
- * keeps fewer bits; above, rows of weight below 2^-126 max(vs) of the largest count as none).  workspace: >= fa_decode_kv4_workspace_bytes(...,
- * weights = acc given); its contents on entry do not matter.  Two launches on `stream`. */
+ * their softmax weight of row j.  A query (rotated, where signs is given) of magnitudes below
+ * 2^110 is taken exactly (22 bits where rotated).  Scales of V from 2^-80 to 2^90 cost no accuracy
+ * (below, o keeps fewer bits; above, a row counts as weightless below 2^-126 max(vs) of the
+ * weightiest).  workspace: >= fa_decode_kv4_workspace_bytes(..., weights = acc given); its
+ * contents on entry do not matter, and calls that may run at the same time need one each.  Two
+ * launches on `stream`. */
 size_t fa_decode_kv4_workspace_bytes(int B, int H, int H_kv, int C, int d, int weights);
 int fa_decode_kv4(const void* q, const void* kc, const void* ks, const void* vc, const void* vs, const float* signs,
                   const int* lens, void* o, float* lse, float* acc, int B, int H, int H_kv, int C, int d, float scale,
