@@ -28,7 +28,7 @@ int launched() {
 // hold fewer blocks; rows of the score buffer padded to an even number of heads.
 struct Kv4Plan {
   int nt, gp, grid, slots;
-  size_t part_o, part_rl, fac, first, scores, bytes;  // offsets in bytes
+  size_t part_o, part_rl, fac, span, scores, bytes;  // offsets in bytes
 };
 
 Kv4Plan kv4_plan(int B, int H, int Hkv, int C, int d, bool weights) {
@@ -44,8 +44,8 @@ Kv4Plan kv4_plan(int B, int H, int Hkv, int C, int d, bool weights) {
   p.part_o = 0;
   p.part_rl = p.part_o + up(static_cast<size_t>(p.slots) * 8 * p.nt * d * 4);
   p.fac = p.part_rl + up(static_cast<size_t>(p.slots) * 8 * p.nt * 8);
-  p.first = p.fac + up(static_cast<size_t>(bhkv) * 8 * p.nt * 4);
-  p.scores = p.first + up((static_cast<size_t>(bhkv) + 1) * 4);
+  p.span = p.fac + up(static_cast<size_t>(bhkv) * 8 * p.nt * 4);
+  p.scores = p.span + up(static_cast<size_t>(bhkv) * 8);
   p.bytes = p.scores + (weights ? up(static_cast<size_t>(bhkv) * C * p.gp * 4) : 0);
   return p;
 }
@@ -91,7 +91,7 @@ int launch_kv4_decode(const fa::Kv4DecodeArgs& a, int nt, cudaStream_t s) {
 // The key weights' plan: CTAs, and the workspace's parts in bytes.
 struct KeyWeightsPlan {
   int ranges, grid;
-  size_t part, first, bytes;
+  size_t part, span, bytes;
 };
 
 KeyWeightsPlan key_weights_plan(int B, int H, int Hkv, int N, int window) {
@@ -102,8 +102,8 @@ KeyWeightsPlan key_weights_plan(int B, int H, int Hkv, int N, int window) {
   p.grid = static_cast<int>(std::min<long long>(148, items * ((subs + 1) / 2)));
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   p.part = 0;
-  p.first = up((static_cast<size_t>(p.grid) + items) * 512 * 4);
-  p.bytes = p.first + up((static_cast<size_t>(B) * p.ranges + 1) * 8);
+  p.span = up((static_cast<size_t>(p.grid) + items) * 512 * 4);
+  p.bytes = p.span + up(static_cast<size_t>(items) * 8);
   return p;
 }
 
@@ -122,8 +122,8 @@ int launch_key_weights(const void* q, const void* k, int B, int H, int Hkv, int 
   kern<<<a.grid, fa::kKeyWeightsThreads, C::SMEM_BYTES, s>>>(mq, mk, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
-  return launch_after(fa::fa_key_weights_sum_kernel, dim3(static_cast<unsigned>(static_cast<long long>(B) * Hkv * a.ranges)),
-                      dim3(256), s, a);
+  const long long items = static_cast<long long>(B) * Hkv * a.ranges;
+  return launch_after(fa::fa_key_weights_sum_kernel, dim3(static_cast<unsigned>((items + 3) / 4)), dim3(256), s, a);
 }
 
 // Eviction: CTAs per head (a cluster of up to eight), while the grid stays within the SMs.
@@ -172,14 +172,14 @@ int fa_key_weights(const void* q, const void* k, const float* lse, float* w, con
     return FA_ERR_ALIGNMENT;
   if (workspace_bytes < fa_key_weights_workspace_bytes(B, H, H_kv, N, d, window)) return FA_ERR_INVALID_ARG;
   const KeyWeightsPlan p = key_weights_plan(B, H, H_kv, N, window);
-  if (static_cast<long long>(B) * H_kv * p.ranges >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * H_kv * p.ranges >= (1ll << 31) - 4) return FA_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   fa::KeyWeightsArgs a;
   a.lse = lse;
   a.w = w;
   a.n_rows = n_rows;
   a.part = reinterpret_cast<float*>(ws + p.part);
-  a.first = reinterpret_cast<long long*>(ws + p.first);
+  a.span = reinterpret_cast<int2*>(ws + p.span);
   a.B = B;
   a.N = N;
   a.ldw = ldw;
@@ -365,7 +365,7 @@ int fa_decode_kv4(const void* q, const void* kc, const void* ks, const void* vc,
   a.part_o = reinterpret_cast<float*>(ws + p.part_o);
   a.part_rl = reinterpret_cast<float2*>(ws + p.part_rl);
   a.fac = reinterpret_cast<float*>(ws + p.fac);
-  a.first = reinterpret_cast<int*>(ws + p.first);
+  a.span = reinterpret_cast<int2*>(ws + p.span);
   a.scores = acc ? reinterpret_cast<float*>(ws + p.scores) : nullptr;
   a.scale_log2 = scale * 1.4426950408889634f / (signs ? static_cast<float>(d) : 1.f);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

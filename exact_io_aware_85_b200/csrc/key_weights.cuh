@@ -42,7 +42,7 @@ struct KeyWeightsArgs {
   float* w;                // [B*Hkv, ldw]
   const int* n_rows;       // [B] or null (N)
   float* part;             // [grid + B*Hkv*ranges, 2, 256]: slot (CTA + item)
-  long long* first;        // [B*ranges + 1]: steps before each (sequence, range), and of them all
+  int2* span;              // [B*Hkv*ranges]: the first and the last CTA that had a part of an item
   int B, N, ldw, H, Hkv, g, window, causal, ranges, grid;
   float scale_log2, neg_inv_scale;
 };
@@ -189,14 +189,6 @@ __global__ void __launch_bounds__(kKeyWeightsThreads, 1)
   const long long total = per_head * a.Hkv;
   const long long n_cta = max(1ll, min(static_cast<long long>(a.grid), total));  // the others have nothing to do
   const long long u0 = min(blockIdx.x * total / n_cta, total), u1 = min((blockIdx.x + 1) * total / n_cta, total);
-  if (blockIdx.x == 0) {
-    long long f = before;
-    for (int e = e0; e < e1; ++e) {
-      a.first[e] = f;
-      f += steps(e);
-    }
-    if (tid == 0) a.first[entries] = per_head;
-  }
   const long long at = per_head > 0 ? u0 % per_head : 0;
   if (u0 < u1 && at >= before && at < before + mine) {
     long long f = before;
@@ -382,6 +374,7 @@ __global__ void __launch_bounds__(kKeyWeightsThreads, 1)
     const float c = a.scale_log2;
     float w = 0.f;
     int cnt = 0;
+    bool begins = cur.h == 0 && cur.tile == 0;
     for (int t = 0; cur.left > 0; ++t) {
       const int k0 = cur.range * 256 + half * 128;
       if ((t & 1) == part && k0 < cur.n) {
@@ -436,6 +429,11 @@ __global__ void __launch_bounds__(kKeyWeightsThreads, 1)
         const long long item = static_cast<long long>(hk) * entries + e;
         a.part[((static_cast<long long>(blockIdx.x) + item) * 2 + part) * 256 + half * 128 + r] = w;
         w = 0.f;
+        if (tid == 0) {
+          if (begins) a.span[item].x = blockIdx.x;
+          if (cur.left > 0 || cur.h >= a.g) a.span[item].y = blockIdx.x;
+        }
+        begins = true;
       }
     }
   }
@@ -448,25 +446,33 @@ __global__ void __launch_bounds__(kKeyWeightsThreads, 1)
 }
 
 // w of 256 keys of one key/value head: the sums of the CTAs that had a part of them, in order.
+// Four keys a thread, four heads' ranges a block (a block each, with the CTAs found by divisions
+// here: 22.7 us instead of 7.0 for 32768 keys in 64 heads, read from DRAM).
 __global__ void __launch_bounds__(256) fa_key_weights_sum_kernel(const KeyWeightsArgs a) {
   const int entries = a.B * a.ranges;
-  const int e = blockIdx.x % entries, hk = blockIdx.x / entries;
-  const int b = e / a.ranges, j = (e % a.ranges) * 256 + threadIdx.x;
+  const int item = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (item >= entries * a.Hkv) return;
+  const int e = item % entries, hk = item / entries, b = e / a.ranges, range = e % a.ranges;
+  const KeyWeightsSeq s = key_weights_seq(a, b);
+  int base;
+  const bool any = key_weights_tiles(a, s, range, base) > 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long per_head = a.first[entries], f = a.first[e];
-  const long long steps = a.first[e + 1] - f;
-  float w = 0.f;
-  if (steps > 0) {
-    const long long total = per_head * a.Hkv, x0 = hk * per_head + f, x1 = x0 + steps;
-    const long long n_cta = min(static_cast<long long>(a.grid), total);
-    const long long i0 = ((x0 + 1) * n_cta - 1) / total, i1 = (x1 * n_cta - 1) / total;
-    for (long long i = i0; i <= i1; ++i) {
-      const float* p = a.part + (i + blockIdx.x) * 512 + threadIdx.x;
-      w += p[0] + p[256];
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  if (any) {
+    const int2 span = a.span[item];
+    const int i0 = max(span.x, 0), i1 = min(span.y, a.grid - 1);  // within the grid, should a wait have given up
+    for (int i = i0; i <= i1; ++i) {
+      const float* const p = a.part + (static_cast<long long>(i) + item) * 512 + lane;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) w[x] += p[64 * x] + p[64 * x + 256];
     }
   }
-  const KeyWeightsSeq s = key_weights_seq(a, b);
-  if (j < a.N) a.w[(static_cast<size_t>(b) * a.Hkv + hk) * a.ldw + j] = j < s.n ? w : 0.f;
+  float* const out = a.w + (static_cast<size_t>(b) * a.Hkv + hk) * a.ldw;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int j = range * 256 + 64 * x + lane;
+    if (j < a.N) out[j] = j < s.n ? w[x] : 0.f;
+  }
 }
 
 }  // namespace fa

@@ -418,7 +418,7 @@ struct Kv4DecodeArgs {
   float* part_o;           // [grid + B*Hkv, 8 NT d]: slot (CTA + head), in the merge's fragment order
   float2* part_rl;         // [grid + B*Hkv, 8 NT]: R, l
   float* fac;              // [B*Hkv, 8 NT]: factors of the scores
-  int* first;              // [B*Hkv + 1]: blocks before each head
+  int2* span;              // [B*Hkv]: the first and the last CTA that worked on a head
   float* scores;           // [B*Hkv, C, gp]: log2 scores less their head's factor, or null
   int C, BHkv, g, gp, grid;
   int stream;              // the cache is larger than the L2
@@ -557,14 +557,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
   const int n_cta = max(1, min(a.grid, total));  // the others have nothing to do
   const int u0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * total / n_cta, static_cast<long long>(total)));
   const int u1 = static_cast<int>(min(static_cast<long long>(blockIdx.x + 1) * total / n_cta, static_cast<long long>(total)));
-  if (blockIdx.x == 0) {
-    int f = before;
-    for (int h = h0; h < h1; ++h) {
-      a.first[h] = f;
-      f += nblocks(kv4_len(a.lens, h, a.C));
-    }
-    if (tid == 0) a.first[a.BHkv] = total;
-  }
   if (u0 >= u1) return;
   int* const start = scan + NW + 1;
   if (u0 >= before && u0 < before + mine) {
@@ -740,6 +732,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
     const int len = cur.len;
     // ================= the head's blocks =================================================
     const int end = min(cur.nblk, cur.blk + left), first = cur.blk;
+    const bool ends = end == cur.nblk;
     left -= end - first;
     if (left > 0) {  // the query of the head after this one (everybody has read qraw)
       next_head();
@@ -1000,6 +993,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
           oacc[j][i][c + 2] = fmaf(oacc[j][i][c + 2], fi, -eight);
         }
       }
+    if (tid == 0 && first == 0) a.span[bh].x = blockIdx.x;
+    if (tid == 0 && ends) a.span[bh].y = blockIdx.x;
     if (tid < NQ) {
       float R = kKv4Lowest, l = 0.f;
       for (int w = 0; w < NW; ++w) R = fmaxf(R, wr[w * NQ + tid]);
@@ -1062,14 +1057,9 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
       }
     }
   }
-  // the CTAs that worked on this head
-  const long long total = a.first[a.BHkv], b0 = a.first[bh], b1 = a.first[bh + 1];
-  int i0 = 0, i1 = -1;
-  if (b1 > b0) {
-    const long long n_cta = min(static_cast<long long>(a.grid), total);
-    i0 = static_cast<int>(((b0 + 1) * n_cta - 1) / total);
-    i1 = static_cast<int>((b1 * n_cta - 1) / total);
-  }
+  // the CTAs that worked on this head (within the grid, should a wait have given up)
+  const int2 span = len > 0 ? a.span[bh] : make_int2(0, -1);
+  const int i0 = max(span.x, 0), i1 = min(span.y, a.grid - 1);
   const float2* const rl = a.part_rl;
   if (tid < NQ) {
     float R = kKv4Lowest, L = 0.f;
