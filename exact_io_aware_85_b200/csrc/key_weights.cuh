@@ -8,7 +8,8 @@
 // keys on the tensor-memory lanes, so that one thread holds one key, and the sum over the
 // queries runs along its registers.  128 keys x 128 queries take the tensor core 512 clocks at
 // d = 128 and the exponential unit 1024, which bounds it: 8192 tokens, 32 heads, causal, d = 128 take
-// 360 us, of which the exponential unit alone needs 245 (68 % busy; the MMAs alone would need 167).
+// 360 to 380 us, of which the exponential unit alone needs 245 (the MMAs alone would need 167).  A
+// window of 64 rows over 8 sequences of 32768 tokens takes 196 us (the unit 119, K from DRAM 88).
 // Computing 1 to 3 of 8 exponentials on the FMA pipe instead (a degree-5 polynomial) made it slower
 // each time it was tried (p. e. 1 of 4: 381 us), as did 8 instead of 16 warps with whole score tiles
 // in registers (460 us).

@@ -48,12 +48,13 @@ struct Kv4AppendArgs {
   int tblocks;             // blocks per (b, head)
 };
 
-// A warp takes 8 rows; lane (grp, tq) holds a quarter of row grp, D/4 elements, as pairs.  The rotation's bits of the element index divide between the tensor core and the
-// registers: bits 0, 1 and the two that name the lane's quarter are the 16 x 16 matrix H16, one
-// m16n8k16 MMA pair per 4 elements (whose operand is the row as it lies in memory, and whose result
-// has the same layout; half of its rows stay empty: two rows a lane took twice the registers and left
-// too few warps to keep the memory busy, 121 us against 118 for the case below); the others are additions between a lane's own pairs.  No shuffles, and a
-// fifth of the instructions of the stages as butterflies.
+// A warp takes 8 rows; lane (grp, tq) holds a quarter of row grp, D/4 elements, as pairs.  The
+// rotation's bits of the element index divide between the tensor core and the registers: bits 0, 1
+// and the two that name the lane's quarter are the 16 x 16 matrix H16, one m16n8k16 MMA pair per 4
+// elements (whose operand is the row as it lies in memory, and whose result has the same layout;
+// half of its rows stay empty: two rows a lane took twice the registers and left too few warps to
+// keep the memory busy, 121 us against 118 for the case below); the others are additions between a
+// lane's own pairs.  No shuffles, and a fifth of the instructions of the stages as butterflies.
 // Append + read of 262144 rows of d = 128 (K and V, 341 MB, 52 us at the copy rate) take 75 us: the
 // butterflies 122 us, this with 16-byte accesses 118, with 32-byte ones 104, without divisions next to
 // a border 87, with eight CTAs per SM (64 registers) 81, K and V of a row read together 75.
@@ -404,6 +405,12 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
 //     maximum of x: rows whose values are zero or tiny keep their share of the sum.
 //   * Work is one list of blocks over all heads' lengths, cut into equal parts, one per CTA:
 //     ragged batches fill the GPU evenly.
+//
+// Measured, both kernels, codes from DRAM: 64 heads of 32768 rows of d = 128, four query heads each,
+// weights wanted: 69 us (the bytes 45 at the copy rate; about 490 instructions per 32 keys keep the
+// issue slots 56 % busy while warps run, of them the scores' store and the weights' kernel cost some
+// 14 us); 64 ragged heads of up to 16384 rows of d = 256, eight query heads each: 48 us (21); 8 heads
+// of 1000 rows of d = 64: 8.4 us, two launches' latency.
 struct Kv4DecodeArgs {
   const __nv_bfloat16* q;  // [B*H, d]
   const float* signs;      // [d] or null
