@@ -67,10 +67,10 @@ int launch_after(void (*kern)(Params...), dim3 grid, dim3 block, cudaStream_t s,
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
-template <int D, int NT, bool TWO>
+template <int D, int NT, bool TWO, bool SPLIT>
 int launch_kv4_decode_as(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
   using L = fa::Kv4Cfg<D, NT>;
-  auto kern = fa::fa_kv4_decode_kernel<D, NT, TWO>;
+  auto kern = fa::fa_kv4_decode_kernel<D, NT, TWO, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
   kern<<<a.grid, L::THREADS, L::BYTES, s>>>(a);
@@ -83,9 +83,10 @@ int launch_kv4_decode_as(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
 
 template <int D>
 int launch_kv4_decode(const fa::Kv4DecodeArgs& a, int nt, cudaStream_t s) {
-  const bool two = a.signs && (a.g > 4);
-  if (nt == 1) return two ? launch_kv4_decode_as<D, 1, true>(a, s) : launch_kv4_decode_as<D, 1, false>(a, s);
-  return two ? launch_kv4_decode_as<D, 2, true>(a, s) : launch_kv4_decode_as<D, 2, false>(a, s);
+  if (a.g <= 4) return launch_kv4_decode_as<D, 1, false, true>(a, s);
+  if (nt == 1)
+    return a.signs ? launch_kv4_decode_as<D, 1, true, false>(a, s) : launch_kv4_decode_as<D, 1, false, false>(a, s);
+  return a.signs ? launch_kv4_decode_as<D, 2, true, false>(a, s) : launch_kv4_decode_as<D, 2, false, false>(a, s);
 }
 
 // The key weights' plan: CTAs, and the workspace's parts in bytes.

@@ -407,10 +407,10 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
 //     ragged batches fill the GPU evenly.
 //
 // Measured, both kernels, codes from DRAM: 64 heads of 32768 rows of d = 128, four query heads each,
-// weights wanted: 69 us (the bytes 45 at the copy rate; about 490 instructions per 32 keys keep the
-// issue slots 56 % busy while warps run, of them the scores' store and the weights' kernel cost some
-// 14 us); 64 ragged heads of up to 16384 rows of d = 256, eight query heads each: 48 us (21); 8 heads
-// of 1000 rows of d = 64: 8.4 us, two launches' latency.
+// weights wanted: 68 us (69 when every lane went on with all 32 keys instead of SPLIT below; the bytes
+// 45 at the copy rate; the issue slots are 56 % busy, and the scores' store and the weights' kernel
+// cost some 13 us); 64 ragged heads of up to 16384 rows of d = 256, eight query heads each: 48 us (21); 8 heads
+// of 1000 rows of d = 64: 8.2 us, two launches' latency.
 struct Kv4DecodeArgs {
   const __nv_bfloat16* q;  // [B*H, d]
   const float* signs;      // [d] or null
@@ -515,8 +515,11 @@ struct Kv4Cursor {
 };
 
 // NT: 8-wide tiles of query heads; TWO: the second halves of a rotated q have MMAs of their own
-// (otherwise, for at most four heads, they sit in the unused columns).
-template <int D, int NT, bool TWO>
+// (otherwise, for at most four heads, they sit in columns 4-7).  SPLIT: at most four heads, so that a
+// score is needed in one of columns n and n + 4 only: the two lanes that hold them add theirs up and
+// go on with one 16-key half each, column n with the first, n + 4 with the second (half the
+// exponentials and what goes with them; the output's two columns are added up at the end).
+template <int D, int NT, bool TWO, bool SPLIT>
 __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kernel(const Kv4DecodeArgs a) {
   using L = Kv4Cfg<D, NT>;
   constexpr int NW = L::NW, ST = L::STAGES, NQ = 8 * NT, WORKERS = NW * 32;
@@ -640,7 +643,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
   }
 
   const bool rotated = a.signs != nullptr;
-  const bool dup = !TWO && rotated;  // second halves of q in columns 4-7
+  constexpr int RW = SPLIT ? 2 : 4;                      // rows of 32 whose scores a lane goes on with
+  const int second = SPLIT ? tq >> 1 : 0;                // and which 16 they belong to
+  const int col = SPLIT ? 2 * (tq & 1) : 2 * tq;         // their columns: col, col + 1 of a tile
   constexpr int EPL = D / 4 < 32 ? D / 4 : 32;    // elements of a lane's chunk of a key
   constexpr float kTwo24 = 16777216.f;
   bool ok = true;
@@ -703,11 +708,11 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
         sum += (e & 1) ? back * 16.f : back;
         const int ks = c * (EPL / 4) + ((r % EPL) >> 3) * 2 + ((e & 3) >> 1);
         const int sub = (e & 1) * 2 + (e >> 2), ql = r / EPL;
-        const int nt = n >> 3, col = n & 7;
-        qf[((((nt * 2) * L::KSTEPS + ks) * 32 + col * 4 + ql) << 2) + sub] = hi;
+        const int nt = n >> 3, nc = n & 7;
+        qf[((((nt * 2) * L::KSTEPS + ks) * 32 + nc * 4 + ql) << 2) + sub] = hi;
         if (rotated) {
-          if (!TWO) qf[((ks * 32 + (col + 4) * 4 + ql) << 2) + sub] = lo;
-          else qf[((((nt * 2 + 1) * L::KSTEPS + ks) * 32 + col * 4 + ql) << 2) + sub] = lo;
+          if (SPLIT) qf[((ks * 32 + (nc + 4) * 4 + ql) << 2) + sub] = lo;
+          else qf[((((nt * 2 + 1) * L::KSTEPS + ks) * 32 + nc * 4 + ql) << 2) + sub] = lo;
         }
       }
 #pragma unroll
@@ -715,7 +720,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
       if (lane == 0) {
         const float f = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 24 - k) << 23);
         fac_sh[n] = f;
-        if (dup) fac_sh[n + 4] = f;
         if (a.scores) a.fac[static_cast<size_t>(bh) * NQ + n] = f;
         fac_sh[NQ + n] = sum * (-8.f / kTwo24);
       }
@@ -726,7 +730,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        fac[j][c] = fac_sh[8 * j + 2 * tq + c];
+        fac[j][c] = fac_sh[8 * j + col + c];
         x0[j][c] = fac_sh[NQ + 8 * j + 2 * tq + c];
         m_run[j][c] = r_run[j][c] = kKv4Lowest;
         l_run[j][c] = 0.f;
@@ -798,71 +802,75 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
               }
             }
         }
-        float vs[4];
+        float y[NT][2 * RW];  // two columns of each row
+        if constexpr (SPLIT) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float mine = second ? x[1][0][i] : x[0][0][i], theirs = second ? x[0][0][i] : x[1][0][i];
+            y[0][i] = mine + __shfl_xor_sync(0xffffffffu, theirs, 2);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[j][i] = x[i >> 2][j][i & 3];
+        }
+        float vs[RW];
+        const int krow = 16 * second + kr;  // the rows are krow + 8 r
         const unsigned short* const ksp =
-            reinterpret_cast<const unsigned short*>(smem + s * L::STAGE + L::OFF_KS) + warp * 32 + kr;
+            reinterpret_cast<const unsigned short*>(smem + s * L::STAGE + L::OFF_KS) + warp * 32 + krow;
         const bool tail = key0 + 32 > len;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < RW; ++r) {
           const float ks = bf16_bits_to_float(ksp[8 * r]);
           vs[r] = bf16_bits_to_float(ksp[L::BLOCK + 8 * r]);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            float& xa = x[r >> 1][j][2 * (r & 1)];
-            float& xb = x[r >> 1][j][2 * (r & 1) + 1];
-            if (NT == 1 && dup) {
-              xa += __shfl_xor_sync(0xffffffffu, xa, 2);
-              xb += __shfl_xor_sync(0xffffffffu, xb, 2);
-            }
-            xa *= ks;
-            xb *= ks;
+            y[j][2 * r] *= ks;
+            y[j][2 * r + 1] *= ks;
           }
         }
         if (tail) {  // rows behind the last hold anything: neither their codes nor their scales count
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (key0 + 8 * r + kr >= len) {
+          for (int r = 0; r < RW; ++r)
+            if (key0 + 8 * r + krow >= len) {
               vs[r] = 0.f;
 #pragma unroll
-              for (int j = 0; j < NT; ++j) x[r >> 1][j][2 * (r & 1)] = x[r >> 1][j][2 * (r & 1) + 1] = -INFINITY;
+              for (int j = 0; j < NT; ++j) y[j][2 * r] = y[j][2 * r + 1] = -INFINITY;
             }
         }
         if (a.scores) {
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            const int n = 8 * j + 2 * tq;
+            const int n = 8 * j + col;
             if (n < g) {
-              float* p = a.scores + (static_cast<size_t>(bh) * a.C + key0 + kr) * a.gp + n;
+              float* p = a.scores + (static_cast<size_t>(bh) * a.C + key0 + krow) * a.gp + n;
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (!tail || key0 + 8 * r + kr < len) {
-                  if (a.gp == 1) p[8 * r] = x[r >> 1][j][2 * (r & 1)];
-                  else *reinterpret_cast<float2*>(p + 8 * r * a.gp) =
-                           make_float2(x[r >> 1][j][2 * (r & 1)], x[r >> 1][j][2 * (r & 1) + 1]);
+              for (int r = 0; r < RW; ++r)
+                if (!tail || key0 + 8 * r + krow < len) {
+                  if (a.gp == 1) p[8 * r] = y[j][2 * r];
+                  else *reinterpret_cast<float2*>(p + 8 * r * a.gp) = make_float2(y[j][2 * r], y[j][2 * r + 1]);
                 }
             }
           }
         }
         // ---- p = 2^(x - R) and u = p vs, x = fac times what is stored; R moves only when a u passes
         // 2^12 (or a p 2^97), and then u is at most 2^8 in the second turn -----------------------------
-        float p[2][NT][4], u[2][NT][4];
+        float p[NT][2 * RW], u[NT][2 * RW];
 #pragma unroll 1
         for (int turn = 0; turn < 2; ++turn) {
           float top_p = 0.f, top_u = 0.f;
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float* const pp = &p[r >> 1][j][2 * (r & 1)];
-              float* const uu = &u[r >> 1][j][2 * (r & 1)];
-              const float* const xx = &x[r >> 1][j][2 * (r & 1)];
+            for (int r = 0; r < RW; ++r) {
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                pp[c] = ex2_approx(fmaf(xx[c], fac[j][c], -r_run[j][c]));
-                uu[c] = pp[c] * vs[r];
+                p[j][2 * r + c] = ex2_approx(fmaf(y[j][2 * r + c], fac[j][c], -r_run[j][c]));
+                u[j][2 * r + c] = p[j][2 * r + c] * vs[r];
               }
-              top_p = fmax3(top_p, pp[0], pp[1]);
-              top_u = fmax3(top_u, uu[0], uu[1]);
+              top_p = fmax3(top_p, p[j][2 * r], p[j][2 * r + 1]);
+              top_u = fmax3(top_u, u[j][2 * r], u[j][2 * r + 1]);
             }
           if (turn || !__any_sync(0xffffffffu, top_p > 1.5845633e29f || top_u > 4096.f)) break;
 #pragma unroll
@@ -872,13 +880,13 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
             for (int c = 0; c < 2; ++c) {
               float mx = -INFINITY, ry = -INFINITY;
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float y = x[r >> 1][j][2 * (r & 1) + c] * fac[j][c];
-                mx = fmaxf(mx, y);
-                ry = fmaxf(ry, y + __log2f(vs[r]));
+              for (int r = 0; r < RW; ++r) {
+                const float z = y[j][2 * r + c] * fac[j][c];
+                mx = fmaxf(mx, z);
+                ry = fmaxf(ry, z + __log2f(vs[r]));
               }
 #pragma unroll
-              for (int off = 4; off < 32; off <<= 1) {
+              for (int off = SPLIT ? 2 : 4; off < 32; off <<= 1) {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                 ry = fmaxf(ry, __shfl_xor_sync(0xffffffffu, ry, off));
               }
@@ -904,15 +912,22 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
         // ---- u as the B operand -----------------------------------------------------------------
         uint32_t pb[2][NT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            l_run[j][0] += p[h][j][0] + p[h][j][2];
-            l_run[j][1] += p[h][j][1] + p[h][j][3];
-            pb[h][j][0] = movmatrix_trans(pack_f16x2(u[h][j][0], u[h][j][1]));
-            pb[h][j][1] = movmatrix_trans(pack_f16x2(u[h][j][2], u[h][j][3]));
+          for (int h = 0; h < RW / 2; ++h) {
+            l_run[j][0] += p[j][4 * h] + p[j][4 * h + 2];
+            l_run[j][1] += p[j][4 * h + 1] + p[j][4 * h + 3];
+            pb[h][j][0] = movmatrix_trans(pack_f16x2(u[j][4 * h], u[j][4 * h + 1]));
+            pb[h][j][1] = movmatrix_trans(pack_f16x2(u[j][4 * h + 2], u[j][4 * h + 3]));
             mma_16816_f16(ones[j], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, pb[h][j][0], pb[h][j][1]);
           }
+        if constexpr (SPLIT) {  // columns 0-3 take the first 16 keys, 4-7 the others
+          const uint32_t mask = grp < 4 ? 0u : 0xffffffffu;
+          pb[1][0][0] = pb[0][0][0] & mask;
+          pb[1][0][1] = pb[0][0][1] & mask;
+          pb[0][0][0] &= ~mask;
+          pb[0][0][1] &= ~mask;
+        }
         // ---- O^T += V^T P^T -----------------------------------------------------------------------
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -974,9 +989,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
       for (int c = 0; c < 2; ++c) {
         float l = l_run[j][c];
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        const int n = 8 * j + 2 * tq + c;
-        if (grp == 0) {
+        for (int off = SPLIT ? 2 : 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        const int n = 8 * j + col + c;
+        if (grp == 0 && !second) {
           wl[warp * NQ + n] = l;
           wr[warp * NQ + n] = r_run[j][c];
         }
@@ -987,7 +1002,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int n = 8 * j + 2 * tq + c;
+        const int n = 8 * j + col + c;
         float R = kKv4Lowest;
 #pragma unroll
         for (int w = 0; w < NW; ++w) R = fmaxf(R, wr[w * NQ + n]);
@@ -998,11 +1013,15 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
           const float fi = (i & 1) ? f * 0.0625f : f;
           oacc[j][i][c] = fmaf(oacc[j][i][c], fi, -eight);
           oacc[j][i][c + 2] = fmaf(oacc[j][i][c + 2], fi, -eight);
+          if constexpr (SPLIT) {
+            oacc[j][i][c] += __shfl_xor_sync(0xffffffffu, oacc[j][i][c], 2);
+            oacc[j][i][c + 2] += __shfl_xor_sync(0xffffffffu, oacc[j][i][c + 2], 2);
+          }
         }
       }
     if (tid == 0 && first == 0) a.span[bh].x = blockIdx.x;
     if (tid == 0 && ends) a.span[bh].y = blockIdx.x;
-    if (tid < NQ) {
+    if (tid < (SPLIT ? 4 : NQ)) {
       float R = kKv4Lowest, l = 0.f;
       for (int w = 0; w < NW; ++w) R = fmaxf(R, wr[w * NQ + tid]);
       for (int w = 0; w < NW; ++w) l += kv4_rescale(wl[w * NQ + tid], wr[w * NQ + tid] - R);
