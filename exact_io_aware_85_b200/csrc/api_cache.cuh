@@ -19,11 +19,6 @@ int check_cache(int B, int Hkv, int C, int d) {
   return FA_OK;
 }
 
-int launched() {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FA_OK : cuda_fail(e);
-}
-
 // The decoding step's plan, from the sizes alone: one CTA per SM (148), fewer when the caches
 // hold fewer blocks; rows of the score buffer padded to an even number of heads.
 struct Kv4Plan {
@@ -51,12 +46,16 @@ Kv4Plan kv4_plan(int B, int H, int Hkv, int C, int d, bool weights) {
 }
 
 // A kernel that is launched while the one before it on the stream still runs, and waits for it
-// on the device (griddepcontrol.wait).
+// on the device: every kernel here begins with wait_for_earlier(), in every thread block, so that
+// a kernel's end is also the end of all kernels before it.  (Calls in a row, launched after the
+// one before has ended: one row of 64 heads to evict 6.3 us instead of 3.7, a token's append and
+// read 10.4 instead of 6.4, a short decoding step 10.4 instead of 8.5.)
 template <typename... Params, typename... Args>
-int launch_after(void (*kern)(Params...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+int launch_after(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -73,12 +72,11 @@ int launch_kv4_decode_as(const fa::Kv4DecodeArgs& a, cudaStream_t s) {
   auto kern = fa::fa_kv4_decode_kernel<D, NT, TWO, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
-  kern<<<a.grid, L::THREADS, L::BYTES, s>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e);
+  const int st = launch_after(kern, dim3(a.grid), dim3(L::THREADS), L::BYTES, s, a);
+  if (st != FA_OK) return st;
   constexpr int KEYS = 4;  // 8: 75 us, 2: 74 us instead of 70 us for 8 x 32768 rows
   const int chunks = a.acc ? (a.C + 256 * KEYS - 1) / (256 * KEYS) : 1;
-  return launch_after(fa::fa_kv4_combine_kernel<D, NT, KEYS>, dim3(chunks, a.BHkv), dim3(256), s, a);
+  return launch_after(fa::fa_kv4_combine_kernel<D, NT, KEYS>, dim3(chunks, a.BHkv), dim3(256), 0, s, a);
 }
 
 template <int D>
@@ -120,11 +118,10 @@ int launch_key_weights(const void* q, const void* k, int B, int H, int Hkv, int 
   auto kern = fa::fa_key_weights_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail(e);
-  kern<<<a.grid, fa::kKeyWeightsThreads, C::SMEM_BYTES, s>>>(mq, mk, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e);
+  if ((st = launch_after(kern, dim3(a.grid), dim3(fa::kKeyWeightsThreads), C::SMEM_BYTES, s, mq, mk, a)) != FA_OK) return st;
   const long long items = static_cast<long long>(B) * Hkv * a.ranges;
-  return launch_after(fa::fa_key_weights_sum_kernel, dim3(static_cast<unsigned>((items + 3) / 4)), dim3(256), s, a);
+  return launch_after(fa::fa_key_weights_sum_kernel, dim3(static_cast<unsigned>((items + 3) / 4)), dim3(256), 0, s,
+                      a);
 }
 
 // Eviction: CTAs per head (a cluster of up to eight), while the grid stays within the SMs.
@@ -137,12 +134,14 @@ int launch_evict(fa::EvictArgs a, int heads, int rows, cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>(heads) * S);
   cfg.blockDim = dim3(1024);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = S;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   const int per = (rows + S - 1) / S;
   const cudaError_t e = per <= 4096   ? cudaLaunchKernelEx(&cfg, fa::fa_evict_kernel<SLOTS, 4>, a)
                         : per <= 8192 ? cudaLaunchKernelEx(&cfg, fa::fa_evict_kernel<SLOTS, 8>, a)
@@ -282,10 +281,9 @@ int fa_kv4_append(const void* k, const void* v, const float* signs, const float*
   if (blocks >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 64) fa::fa_kv4_append_kernel<64><<<grid, 128, 0, s>>>(a);
-  else if (d == 128) fa::fa_kv4_append_kernel<128><<<grid, 128, 0, s>>>(a);
-  else fa::fa_kv4_append_kernel<256><<<grid, 128, 0, s>>>(a);
-  return launched();
+  if (d == 64) return launch_after(fa::fa_kv4_append_kernel<64>, grid, dim3(128), 0, s, a);
+  if (d == 128) return launch_after(fa::fa_kv4_append_kernel<128>, grid, dim3(128), 0, s, a);
+  return launch_after(fa::fa_kv4_append_kernel<256>, grid, dim3(128), 0, s, a);
 }
 
 int fa_kv4_read(const void* kc, const void* ks, const void* vc, const void* vs, const float* signs, const int* slots,
@@ -317,10 +315,9 @@ int fa_kv4_read(const void* kc, const void* ks, const void* vc, const void* vs, 
   if (blocks >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   const unsigned grid = static_cast<unsigned>(blocks);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 64) fa::fa_kv4_read_kernel<64><<<grid, 128, 0, s>>>(a);
-  else if (d == 128) fa::fa_kv4_read_kernel<128><<<grid, 128, 0, s>>>(a);
-  else fa::fa_kv4_read_kernel<256><<<grid, 128, 0, s>>>(a);
-  return launched();
+  if (d == 64) return launch_after(fa::fa_kv4_read_kernel<64>, dim3(grid), dim3(128), 0, s, a);
+  if (d == 128) return launch_after(fa::fa_kv4_read_kernel<128>, dim3(grid), dim3(128), 0, s, a);
+  return launch_after(fa::fa_kv4_read_kernel<256>, dim3(grid), dim3(128), 0, s, a);
 }
 
 size_t fa_decode_kv4_workspace_bytes(int B, int H, int H_kv, int C, int d, int weights) {

@@ -17,8 +17,8 @@
 // A cluster barrier takes a microsecond and distributed shared memory gives an SM some 16 bytes a
 // clock, so a head gets CTAs only while the grid stays within the SMs (64 heads of 32768 rows with
 // all three digits counted over all rows: 128 CTAs 18.3 us, 256 CTAs 27 us, 64 CTAs 40 us).
-// Measured: 4096 of 32768 rows in 64 heads 17.4 us, 512 of 131000 rows in 8 heads 17.7 us (24 us
-// with three counted digits and ranks by ballots), one of 4096 rows in 64 heads 3.8 us.
+// Measured: 4096 of 32768 rows in 64 heads 17 us, 512 of 131000 rows in 8 heads 18 us (24 us
+// with three counted digits and ranks by ballots), one of 4096 rows in 64 heads 3.5 us.
 // One row to take (a decoding step of a full cache) needs no search: one reduction over
 // (key, row) pairs.
 #pragma once
@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(1024) fa_evict_kernel(const EvictArgs a) {
     if (S > 1) cluster_sync_all();
     else __syncthreads();
   };
+  wait_for_earlier();
   int len, n;  // rows looked at, rows to take
   int free_rows = 0, recent_from = 0;
   if (SLOTS) {

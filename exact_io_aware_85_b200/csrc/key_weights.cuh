@@ -9,7 +9,7 @@
 // queries runs along its registers.  128 keys x 128 queries take the tensor core 512 clocks at
 // d = 128 and the exponential unit 1024, which bounds it: 8192 tokens, 32 heads, causal, d = 128 take
 // 360 to 380 us, of which the exponential unit alone needs 245 (the MMAs alone would need 167).  A
-// window of 64 rows over 8 sequences of 32768 tokens takes 196 us (the unit 119, K from DRAM 88).
+// window of 64 rows over 8 sequences of 32768 tokens takes 193 us (the unit 119, K from DRAM 88).
 // Computing 1 to 3 of 8 exponentials on the FMA pipe instead (a degree-5 polynomial) made it slower
 // each time it was tried (p. e. 1 of 4: 381 us), as did 8 instead of 16 warps with whole score tiles
 // in registers (460 us).
@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(kKeyWeightsThreads, 1)
   __shared__ long long start_rem;
   __shared__ int start_e;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  asm volatile("griddepcontrol.launch_dependents;");
   if (warp == 17) {
     tmem_alloc(&tmem_base_sh, 512);
     tmem_relinquish();
@@ -163,6 +162,7 @@ __global__ void __launch_bounds__(kKeyWeightsThreads, 1)
     reinterpret_cast<uint4*>(smem + C::OFF_X)[i] = one ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
   }
   fence_proxy_async_smem();
+  wait_for_earlier();
   // ---- this CTA's part of the list ------------------------------------------------------
   const int entries = a.B * a.ranges;
   const int per = (entries + kKeyWeightsThreads - 1) / kKeyWeightsThreads;
@@ -452,12 +452,12 @@ __global__ void __launch_bounds__(kKeyWeightsThreads, 1)
 __global__ void __launch_bounds__(256) fa_key_weights_sum_kernel(const KeyWeightsArgs a) {
   const int entries = a.B * a.ranges;
   const int item = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  wait_for_earlier();
   if (item >= entries * a.Hkv) return;
   const int e = item % entries, hk = item / entries, b = e / a.ranges, range = e % a.ranges;
   const KeyWeightsSeq s = key_weights_seq(a, b);
   int base;
   const bool any = key_weights_tiles(a, s, range, base) > 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   float w[4] = {0.f, 0.f, 0.f, 0.f};
   if (any) {
     const int2 span = a.span[item];

@@ -118,6 +118,7 @@ __device__ __forceinline__ void kv4_sign_masks(const float* signs, uint32_t* mas
 template <int D>
 __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_kv4_append_kernel(const Kv4AppendArgs a) {
   using R = Kv4Rows<D>;
+  wait_for_earlier();
   __shared__ __align__(16) uint32_t masks[D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane >> 2, tq = lane & 3;
   const int bh = blockIdx.x / a.tblocks;
@@ -268,6 +269,7 @@ struct Kv4ReadArgs {
 template <int D>
 __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_kv4_read_kernel(const Kv4ReadArgs a) {
   using R = Kv4Rows<D>;
+  wait_for_earlier();
   __shared__ __align__(16) uint32_t masks[D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane >> 2, tq = lane & 3;
   const int bh = blockIdx.x / a.tblocks;
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
 // each, weights wanted: 68 us (69 when every lane went on with all 32 keys instead of SPLIT below;
 // the bytes 45 at the copy rate; the issue slots are 56 % busy, and the scores' store and the
 // weights' kernel cost some 13 us); 64 ragged heads of up to 16384 rows of d = 256, eight query
-// heads each: 48 us (21); 8 heads of 1000 rows of d = 64: 8.2 us, two launches' latency.
+// heads each: 48 us (21); 8 heads of 1000 rows of d = 64: 8 us, two launches' latency.
 struct Kv4DecodeArgs {
   const __nv_bfloat16* q;  // [B*H, d]
   const float* signs;      // [d] or null
@@ -536,7 +538,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
   float* const wr = wl + NW * NQ;
   __nv_bfloat16* const qraw = reinterpret_cast<__nv_bfloat16*>(smem + L::OFF_QRAW);
   float* const sign_sh = reinterpret_cast<float*>(smem + L::OFF_SIGN);
-  asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) {
     *abort_sh = 0;
     for (int s = 0; s < ST; ++s) {
@@ -545,6 +546,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
     }
     fence_mbar_init();
   }
+  wait_for_earlier();
   // ---- this CTA's part of the list of blocks -------------------------------------------
   const int per = (a.BHkv + L::THREADS - 1) / L::THREADS;
   const int h0 = min(a.BHkv, tid * per), h1 = min(a.BHkv, h0 + per);
@@ -1057,10 +1059,10 @@ __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const Kv4DecodeArgs
   constexpr int NQ = 8 * NT, MT = D / 16, CHUNK = 256 * KEYS;
   __shared__ float lse2[NQ], fac[NQ];
   const int bh = blockIdx.y, g = a.g, tid = threadIdx.x, gp = a.gp;
-  const int len = kv4_len(a.lens, bh, a.C);
   const int key0 = blockIdx.x * CHUNK + tid;
+  wait_for_earlier();
+  const int len = kv4_len(a.lens, bh, a.C);
   if (blockIdx.x > 0 && blockIdx.x * CHUNK >= len) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const size_t row = static_cast<size_t>(bh) * a.C + key0;
   float old[KEYS];
   float2 sc[KEYS][2];  // the first four heads' scores

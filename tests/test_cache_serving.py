@@ -83,3 +83,133 @@ def test_prompt_then_tokens(B, H, Hkv, N, budget, d, rot, graph):
         assert ((ot.cpu().double() - ro).abs() <= 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2.0 ** -12) * pv).all()
         assert ((lt.cpu().double() - rl).abs() <= 2.0 ** -12).all()
         assert ((acc.cpu().double() - acc0.double() - rw).abs() <= 2.0 ** -11 * rw + 2.0 ** -22 * (acc0 + 1)).all()
+
+
+@pytest.mark.parametrize("how", ["queued", "graph"])
+def test_calls_wait_for_one_another(how):
+    """The kernels come onto the GPU while those before them still run: a layer-like chain of calls whose inputs
+    are written just before by slow kernels gives the bits of the same calls with a synchronisation after each."""
+    from exact_io_aware_85_b200 import fa
+    B, H, Hkv, N, C, d, T = 2, 8, 2, 640, 384, 128, 12
+    g = torch.Generator().manual_seed(3)
+    rnd = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    q, k, v, qt = rnd(B, H, N, d), rnd(B, Hkv, N, d), rnd(B, Hkv, N, d), rnd(B, H, d)
+    signs = (torch.randint(0, 2, (d,), generator=g) * 2 - 1).float().to(DEV)
+    big = rnd(4096, 4096)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    scale = 1 / math.sqrt(d)
+    wsk = torch.empty(fa.fa_key_weights_workspace_bytes(B, H, Hkv, N, d, 100), dtype=torch.uint8, device=DEV)
+    wsd = torch.empty(fa.fa_decode_kv4_workspace_bytes(B, H, Hkv, C, d, True), dtype=torch.uint8, device=DEV)
+
+    def state():
+        z = lambda *s, t=torch.float32: torch.zeros(s, dtype=t, device=DEV)  # noqa: E731
+        bf = torch.bfloat16
+        return dict(q=z(B, H, N, d, t=bf), k=z(B, Hkv, N, d, t=bf), v=z(B, Hkv, N, d, t=bf), o=z(B, H, N, d, t=bf), lse=z(B, H, N),
+                    w=z(B, Hkv, N), idx=z(B, Hkv, 300, t=torch.int32), lens=z(B, Hkv, t=torch.int32), acc=z(B, Hkv, C),
+                    pos=z(B, Hkv, C, t=torch.int32), seen=torch.full((B,), N, **i32), slots=z(B, Hkv, 2, t=torch.int32),
+                    cache=[z(B, Hkv, C, d // 2, t=torch.uint8), z(B, Hkv, C, t=bf), z(B, Hkv, C, d // 2, t=torch.uint8), z(B, Hkv, C, t=bf)],
+                    qt=z(B, H, d, t=bf), kt=z(B, Hkv, 2, d, t=bf), vt=z(B, Hkv, 2, d, t=bf), ot=z(B, H, d, t=bf), lt=z(B, H),
+                    kr=z(B, Hkv, C, d, t=bf), vr=z(B, Hkv, C, d, t=bf), tmp=torch.empty_like(big))
+
+    def chain(s, wait):
+        torch.mm(big, big, out=s["tmp"])  # what follows queues behind it
+        for x, y in (("q", q), ("k", k), ("v", v), ("qt", qt)):
+            s[x].copy_(y)
+        wait()
+        fa.fa_fwd_gqa(s["q"], s["k"], s["v"], s["o"], s["lse"], True, scale)
+        wait()
+        fa.fa_key_weights(s["q"], s["k"], s["lse"], s["w"], True, scale, wsk, window=100)
+        wait()
+        fa.fa_evict_keep(s["w"], s["idx"], s["lens"], 16, 4)
+        wait()
+        fa.fa_kv4_append(s["k"], s["v"], *s["cache"], signs=signs, rows=s["idx"], w=s["w"], acc=s["acc"], pos=s["pos"])
+        wait()
+        for t in range(T):
+            s["kt"].copy_(k[:, :, 2 * t:2 * t + 2])
+            s["vt"].copy_(v[:, :, 2 * t:2 * t + 2])
+            wait()
+            fa.fa_evict_slots(s["acc"], s["pos"], s["lens"], s["seen"], s["slots"], 310, 16, 4)
+            wait()
+            fa.fa_kv4_append(s["kt"], s["vt"], *s["cache"], signs=signs, slots=s["slots"], acc=s["acc"], pos=s["pos"], base=s["seen"])
+            wait()
+            fa.fa_decode_kv4(s["qt"], *s["cache"], s["lens"], s["ot"], s["lt"], scale, wsd, signs=signs, acc=s["acc"])
+            wait()
+            s["qt"].copy_(s["ot"])
+            s["seen"].add_(2)
+            wait()
+        fa.fa_kv4_read(*s["cache"], s["kr"], s["vr"], signs=signs, lens=s["lens"])
+        wait()
+
+    want = state()
+    chain(want, torch.cuda.synchronize)
+    got = state()
+    if how == "graph":
+        run = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(run):
+            chain(got, lambda: None)
+        run.replay()
+    else:
+        chain(got, lambda: None)
+    torch.cuda.synchronize()
+    assert fa.fa_check_status() == fa.FA_OK
+    for name, x in want.items():
+        if name != "tmp":
+            for a, b in zip(x if isinstance(x, list) else [x], got[name] if isinstance(x, list) else [got[name]]):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+    assert bool((want["lens"] == 310).all()) and bool(want["ot"].float().abs().sum() > 0)
+
+
+@pytest.mark.parametrize("how", ["queued", "graph"])
+def test_calls_wait_for_other_streams(how):
+    """A call behind one of its own kind and behind an event of another stream, on which its inputs are written late."""
+    from exact_io_aware_85_b200 import fa
+    B, H, Hkv, C, d = 2, 8, 2, 256, 128
+    g = torch.Generator().manual_seed(4)
+    rnd = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    k, v, q, big = rnd(B, Hkv, C, d), rnd(B, Hkv, C, d), rnd(B, H, d), rnd(4096, 4096)
+    ws = torch.empty(fa.fa_decode_kv4_workspace_bytes(B, H, Hkv, C, d, False), dtype=torch.uint8, device=DEV)
+    lens = torch.full((B, Hkv), C, dtype=torch.int32, device=DEV)
+
+    def state():
+        cache = [torch.zeros((B, Hkv, C, d // 2), dtype=torch.uint8, device=DEV), torch.zeros((B, Hkv, C), dtype=torch.bfloat16, device=DEV)]
+        return dict(k=torch.zeros_like(k), v=torch.zeros_like(v), q=torch.zeros_like(q), o=torch.zeros_like(q),
+                    lse=torch.zeros((B, H), device=DEV), cache=cache + [t.clone() for t in cache], tmp=torch.empty_like(big))
+
+    def chain(s, side):
+        main = torch.cuda.current_stream()
+        fa.fa_kv4_append(s["k"], s["v"], *s["cache"])  # zeros
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.mm(big, big, out=s["tmp"])
+            s["k"].copy_(k)
+            s["v"].copy_(v)
+        fa.fa_decode_kv4(s["q"], *s["cache"], lens, s["o"], s["lse"], 0.1, ws)
+        main.wait_stream(side)
+        fa.fa_kv4_append(s["k"], s["v"], *s["cache"])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.mm(big, big, out=s["tmp"])
+            s["q"].copy_(q)
+        fa.fa_kv4_append(s["k"], s["v"], *s["cache"])
+        main.wait_stream(side)
+        fa.fa_decode_kv4(s["q"], *s["cache"], lens, s["o"], s["lse"], 0.1, ws)
+
+    want = state()
+    want["k"].copy_(k), want["v"].copy_(v), want["q"].copy_(q)
+    fa.fa_kv4_append(want["k"], want["v"], *want["cache"])
+    torch.cuda.synchronize()
+    fa.fa_decode_kv4(want["q"], *want["cache"], lens, want["o"], want["lse"], 0.1, ws)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got, side = state(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        if how == "graph":
+            run = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(run):
+                chain(got, side)
+            run.replay()
+        else:
+            chain(got, side)
+        torch.cuda.synchronize()
+        for a, b in zip([want["o"], want["lse"], *want["cache"]], [got["o"], got["lse"], *got["cache"]]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
