@@ -720,7 +720,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1) fa_kv4_decode_kerne
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       if (lane == 0) {
-        const float f = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 24 - k) << 23);
+        // never 0 (a scale below 2^-54 with a query of zeros): rows behind the last get the score -infinity,
+        // which has to stay one times f.  2^-149 instead of 0 moves a score, 2^127 f at most, by 2^-22.
+        const float f = fmaxf(a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 24 - k) << 23), __uint_as_float(1u));
         fac_sh[n] = f;
         if (a.scores) a.fac[static_cast<size_t>(bh) * NQ + n] = f;
         fac_sh[NQ + n] = sum * (-8.f / kTwo24);
