@@ -3,11 +3,14 @@
 Argument marshalling only: sizes and raw device pointers are taken from torch
 tensors (torch is the allocator and stream owner), every step of the
 computation runs in the library's CUDA kernels.  There is no fallback: if the
-library is missing the import fails, and a non-zero status raises FAError.
+library is missing the import fails, and a non-zero status raises FAError.  The
+operators of the 4-bit cache are called through an extension module (_fa_call);
+where that is missing, they and nothing else raise ImportError.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 import torch
@@ -19,10 +22,22 @@ if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{os.path.basename(_LIB_PATH)} is not built ({_LIB_PATH}); run "
                       f"`python -m exact_io_aware_85_b200.build{' --debug' if _DEBUG else ''}`")
 
+
+class _Unloaded:
+    """Stands for _fa_call.so where it cannot be loaded: a call through it says why."""
+
+    def __init__(self, why: ImportError):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the cache operators need _fa_call.so, which did not load ({self.why}); run "
+                          "`python -m exact_io_aware_85_b200.build`") from self.why
+
+
 try:
-    from . import _fa_call  # argument marshalling of the cache operators
+    _fa_call = importlib.import_module("._fa_call", __package__)  # argument marshalling of the cache operators
 except ImportError as e:
-    raise ImportError("_fa_call.so is not built; run `python -m exact_io_aware_85_b200.build`") from e
+    _fa_call = _Unloaded(e)
 
 lib = ctypes.CDLL(_LIB_PATH)
 _vp, _ci, _cf, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -300,8 +315,9 @@ lib.fa_decode_kv4_workspace_bytes.restype = _sz
 lib.fa_decode_kv4_workspace_bytes.argtypes = [_ci] * 6
 lib.fa_decode_kv4.argtypes = [_vp] * 10 + [_ci] * 5 + [_cf, _vp, _sz, _vp]
 _i32 = torch.int32
-_fa_call.bind(*(ctypes.cast(getattr(lib, name), _vp).value for name in (
-    "fa_key_weights", "fa_evict_keep", "fa_evict_slots", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4")))
+if not isinstance(_fa_call, _Unloaded):
+    _fa_call.bind(*(ctypes.cast(getattr(lib, name), _vp).value for name in (
+        "fa_key_weights", "fa_evict_keep", "fa_evict_slots", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4")))
 
 
 def _done(status: int, where: str, *tensors) -> None:
