@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import os
 import subprocess
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -58,11 +59,16 @@ def build_call(force: bool = False) -> str:
 
 
 def build_library(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
+    """The C library, which needs nvcc alone; then, where torch, its headers and Python's are there, the
+    binding's extension module (without it the binding lacks the cache operators; build_call() says why)."""
     out = LIB_DEBUG if debug else LIB
-    build_call(force)
     if force or needs_build(out):
         extra = (("-Xptxas", "-v") if verbose else ()) + (("-DFA_DEBUG",) if debug else ())
         subprocess.run(nvcc_command(out=out, extra=extra), check=True)
+    try:
+        build_call(force)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"_fa_call.so, which the cache operators' Python calls need, is not built: {e}")
     return out
 
 
