@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import os
 import subprocess
+import sys
 import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +18,7 @@ LIB_DEBUG = os.path.join(PKG, "libfa_debug.so")
 SOURCES = ["api.cu", "sm100.cuh", "fwd.cuh", "bwd.cuh", "fp8.cuh", "decode.cuh", "fwd256.cuh", "bwd256.cuh",
            "kv4.cuh", "evict.cuh", "key_weights.cuh", "api_cache.cuh"]
 CALL = os.path.join(PKG, "_fa_call.so")  # the cache operators' argument marshalling (csrc/call.cpp)
+CALL_STAMP = os.path.join(PKG, "_fa_call.stamp")  # what it was built with
 HEADER = os.path.join(os.path.dirname(PKG), "include", "fa.h")
 
 
@@ -49,12 +51,36 @@ def call_command(out: str = CALL):
             "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
 
 
+def _call_made_with() -> str:
+    import torch
+
+    return f"torch {torch.__version__}, Python {sys.version}"
+
+
+def needs_build_call() -> bool:
+    deps = (os.path.join(CSRC, "call.cpp"), HEADER, os.path.abspath(__file__))
+    try:
+        with open(CALL_STAMP) as f:
+            made_with = f.read()
+        t = os.path.getmtime(CALL)
+    except FileNotFoundError:
+        return True
+    return made_with != _call_made_with() or any(os.path.getmtime(p) > t for p in deps)
+
+
 def build_call(force: bool = False) -> str:
-    src = os.path.join(CSRC, "call.cpp")
-    if force or not os.path.exists(CALL) or os.path.getmtime(src) > os.path.getmtime(CALL):
+    """_fa_call.so.  One that is out of date goes before the next is built: it passes arguments by position, and
+    links against one torch."""
+    made_with = _call_made_with()
+    if force or needs_build_call():
+        for path in (CALL_STAMP, CALL):
+            if os.path.exists(path):
+                os.remove(path)
         tmp = f"{CALL}.{os.getpid()}"
         subprocess.run(call_command(tmp), check=True)
         os.replace(tmp, CALL)
+        with open(CALL_STAMP, "w") as f:
+            f.write(made_with)
     return CALL
 
 
@@ -73,6 +99,5 @@ def build_library(force: bool = False, verbose: bool = False, debug: bool = Fals
 
 
 if __name__ == "__main__":
-    import sys
     dbg = "--debug" in sys.argv
     print(build_library(force=True, verbose=True, debug=dbg))

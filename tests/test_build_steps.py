@@ -47,3 +47,68 @@ def test_the_library_needs_nvcc_alone(tmp_path, lacks):
     r = subprocess.run([sys.executable, "-c", _SCRIPT, str(tmp_path), lacks], env=env, cwd=str(tmp_path), capture_output=True,
                        text=True, timeout=300)
     assert r.returncode == 0 and "refused" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.fixture
+def step(tmp_path, monkeypatch):
+    """The build step of a copy whose module compiler writes a word; `step()` tells whether it was called."""
+    import importlib.util
+    _package(tmp_path)
+    spec = importlib.util.spec_from_file_location("build_copy", tmp_path / "exact_io_aware_85_b200" / "build.py")
+    build = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(build)
+    calls, ok = [], [True]
+
+    def run(cmd, check):
+        calls.append(cmd)
+        if not ok[0]:
+            raise subprocess.CalledProcessError(1, cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("module")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+
+    def go():
+        n = len(calls)
+        build.build_call()
+        return len(calls) > n
+
+    go.build, go.ok = build, ok
+    return go
+
+
+def _older(path, than):
+    t = os.path.getmtime(than) - 10
+    os.utime(path, (t, t))
+
+
+def test_the_module_follows_what_it_is_made_of(step):
+    """It is called by hand-made signatures and linked against torch: built again when its source, the header or
+    the build step are newer, and under another torch or Python."""
+    import torch
+    build = step.build
+    assert step() and not step()
+    for path in (os.path.join(build.CSRC, "call.cpp"), build.HEADER, build.__file__):
+        _older(build.CALL, path)
+        assert step() and not step(), path
+    for name in ("torch.__version__", "sys.version"):
+        with pytest.MonkeyPatch.context() as m:
+            if name == "sys.version":
+                m.setattr(sys, "version", "4.0.0 of another day")
+            else:
+                m.setattr(torch, "__version__", "3.0.0+of_another_day")
+            assert step() and not step(), name
+        assert step() and not step(), name
+
+
+def test_a_module_that_could_not_be_built_again_is_gone(step):
+    """The one from before would be called with arguments in other places."""
+    build = step.build
+    assert step()
+    _older(build.CALL, build.HEADER)
+    step.ok[0] = False
+    with pytest.raises(subprocess.CalledProcessError):
+        step()
+    assert not os.path.exists(build.CALL)
+    step.ok[0] = True
+    assert step() and not step()
