@@ -14,15 +14,28 @@
 #include <cstdint>
 #include <initializer_list>
 
+#include "../../include/fa.h"
+
 namespace {
 
 void* g_fn[6];  // addresses of the library's entry points, in the order of `bind`
 enum { kKeyWeights, kEvictKeep, kEvictSlots, kAppend, kRead, kDecode };
+// one of them, called by its prototype in fa.h
+#define FA_ENTRY(i, f) reinterpret_cast<decltype(&f)>(g_fn[i])
 
 constexpr auto BF16 = at::ScalarType::BFloat16;
 constexpr auto F32 = at::ScalarType::Float;
 constexpr auto U8 = at::ScalarType::Byte;
 constexpr auto I32 = at::ScalarType::Int;
+
+// A checked tensor's memory, as whatever the entry point's prototype says.
+struct Ptr {
+  void* p = nullptr;
+  template <typename T>
+  operator T*() const {
+    return static_cast<T*>(p);
+  }
+};
 
 // One call's view of its arguments: `bad` once any of them does not fit.
 struct Call {
@@ -43,18 +56,18 @@ struct Call {
     }
     return t;
   }
-  void* get(int i, at::ScalarType type, std::initializer_list<int64_t> shape, bool required) {
+  Ptr get(int i, at::ScalarType type, std::initializer_list<int64_t> shape, bool required) {
     if (args[i] == Py_None) {
       bad = bad || required;
-      return nullptr;
+      return {};
     }
     const at::Tensor* t = tensor(i);
     if (!t || t->scalar_type() != type || !t->is_cuda() || t->get_device() != dev || !t->is_contiguous() ||
         !t->sizes().equals(c10::IntArrayRef(shape))) {
       bad = true;
-      return nullptr;
+      return {};
     }
-    return t->data_ptr();
+    return {t->data_ptr()};
   }
   double number(int i) {
     const double v = PyFloat_AsDouble(args[i]);
@@ -108,15 +121,14 @@ PyObject* key_weights(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor *q = c.shaped(0, 4), *k = c.shaped(1, 4), *w = c.shaped(3, 3), *ws = c.shaped(5, 1);
     if (c.bad) return -1;
     const int64_t B = q->size(0), H = q->size(1), N = q->size(2), d = q->size(3), Hkv = k->size(1), ldw = w->size(2);
-    void* p[6] = {c.get(0, BF16, {B, H, N, d}, true), c.get(1, BF16, {B, Hkv, N, d}, true), c.get(2, F32, {B, H, N}, true),
-                  c.get(3, F32, {B, Hkv, ldw}, true), c.get(4, I32, {B}, false), c.get(5, U8, {ws->size(0)}, true)};
+    Ptr p[6] = {c.get(0, BF16, {B, H, N, d}, true), c.get(1, BF16, {B, Hkv, N, d}, true), c.get(2, F32, {B, H, N}, true),
+                c.get(3, F32, {B, Hkv, ldw}, true), c.get(4, I32, {B}, false), c.get(5, U8, {ws->size(0)}, true)};
     const int causal = c.truth(6);
     const int window = c.args[7] == Py_None ? static_cast<int>(N) : c.integer(7);
     const float scale = static_cast<float>(c.number(8));
     if (c.bad || !fits_int({B, H, Hkv, N, ldw, d})) return -1;
-    using Fn = int (*)(void*, void*, void*, void*, void*, int, int, int, int, int, int, int, int, float, void*, size_t, void*);
-    return reinterpret_cast<Fn>(g_fn[kKeyWeights])(p[0], p[1], p[2], p[3], p[4], B, H, Hkv, N, ldw, d, causal, window, scale,
-                                                   p[5], ws->size(0), c.stream(9));
+    return FA_ENTRY(kKeyWeights, fa_key_weights)(p[0], p[1], p[2], p[3], p[4], B, H, Hkv, N, ldw, d, causal, window, scale,
+                                                 p[5], ws->size(0), c.stream(9));
   });
 }
 
@@ -126,12 +138,11 @@ PyObject* evict_keep(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor *w = c.shaped(0, 3), *idx = c.shaped(2, 3);
     if (c.bad) return -1;
     const int64_t B = w->size(0), Hkv = w->size(1), C = w->size(2), keep = idx->size(2);
-    void* p[4] = {c.get(0, F32, {B, Hkv, C}, true), c.get(1, I32, {B, Hkv}, false), c.get(2, I32, {B, Hkv, keep}, true),
-                  c.get(3, I32, {B, Hkv}, true)};
+    Ptr p[4] = {c.get(0, F32, {B, Hkv, C}, true), c.get(1, I32, {B, Hkv}, false), c.get(2, I32, {B, Hkv, keep}, true),
+                c.get(3, I32, {B, Hkv}, true)};
     const int recent = c.integer(4), sink = c.integer(5);
     if (c.bad || !fits_int({B, Hkv, C, keep})) return -1;
-    using Fn = int (*)(void*, void*, void*, void*, int, int, int, int, int, int, void*);
-    return reinterpret_cast<Fn>(g_fn[kEvictKeep])(p[0], p[1], p[2], p[3], B, Hkv, C, keep, recent, sink, c.stream(6));
+    return FA_ENTRY(kEvictKeep, fa_evict_keep)(p[0], p[1], p[2], p[3], B, Hkv, C, keep, recent, sink, c.stream(6));
   });
 }
 
@@ -141,13 +152,12 @@ PyObject* evict_slots(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor *acc = c.shaped(0, 3), *slots = c.shaped(4, 3);
     if (c.bad) return -1;
     const int64_t B = acc->size(0), Hkv = acc->size(1), C = acc->size(2), T = slots->size(2);
-    void* p[5] = {c.get(0, F32, {B, Hkv, C}, true), c.get(1, I32, {B, Hkv, C}, true), c.get(2, I32, {B, Hkv}, true),
-                  c.get(3, I32, {B}, true), c.get(4, I32, {B, Hkv, T}, true)};
+    Ptr p[5] = {c.get(0, F32, {B, Hkv, C}, true), c.get(1, I32, {B, Hkv, C}, true), c.get(2, I32, {B, Hkv}, true),
+                c.get(3, I32, {B}, true), c.get(4, I32, {B, Hkv, T}, true)};
     const int budget = c.integer(5), recent = c.integer(6), sink = c.integer(7);
     if (c.bad || !fits_int({B, Hkv, C, T})) return -1;
-    using Fn = int (*)(void*, void*, void*, void*, void*, int, int, int, int, int, int, int, void*);
-    return reinterpret_cast<Fn>(g_fn[kEvictSlots])(p[0], p[1], p[2], p[3], p[4], B, Hkv, C, budget, T, recent, sink,
-                                                   c.stream(8));
+    return FA_ENTRY(kEvictSlots, fa_evict_slots)(p[0], p[1], p[2], p[3], p[4], B, Hkv, C, budget, T, recent, sink,
+                                                 c.stream(8));
   });
 }
 
@@ -170,19 +180,17 @@ PyObject* kv4_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
       if (t) ldw = t->size(2);
     }
     if (c.bad) return -1;
-    void* p[15] = {c.get(0, BF16, {B, Hkv, N, d}, true), c.get(1, BF16, {B, Hkv, N, d}, true),
-                   c.get(2, F32, {d}, false),            c.get(3, F32, {B, Hkv, ldw}, false),
-                   c.get(4, I32, {B, Hkv, T}, false),    c.get(5, I32, {B, Hkv, T}, false),
-                   c.get(6, I32, {B, Hkv}, false),       c.get(7, I32, {B, Hkv}, false),
-                   c.get(8, I32, {B}, false),            c.get(9, U8, {B, Hkv, C, half}, true),
-                   c.get(10, BF16, {B, Hkv, C}, true),   c.get(11, U8, {B, Hkv, C, half}, true),
-                   c.get(12, BF16, {B, Hkv, C}, true),   c.get(13, F32, {B, Hkv, C}, false),
-                   c.get(14, I32, {B, Hkv, C}, false)};
+    Ptr p[15] = {c.get(0, BF16, {B, Hkv, N, d}, true), c.get(1, BF16, {B, Hkv, N, d}, true),
+                 c.get(2, F32, {d}, false),            c.get(3, F32, {B, Hkv, ldw}, false),
+                 c.get(4, I32, {B, Hkv, T}, false),    c.get(5, I32, {B, Hkv, T}, false),
+                 c.get(6, I32, {B, Hkv}, false),       c.get(7, I32, {B, Hkv}, false),
+                 c.get(8, I32, {B}, false),            c.get(9, U8, {B, Hkv, C, half}, true),
+                 c.get(10, BF16, {B, Hkv, C}, true),   c.get(11, U8, {B, Hkv, C, half}, true),
+                 c.get(12, BF16, {B, Hkv, C}, true),   c.get(13, F32, {B, Hkv, C}, false),
+                 c.get(14, I32, {B, Hkv, C}, false)};
     if (c.bad || !fits_int({B, Hkv, N, T, C, ldw, d})) return -1;
-    using Fn = int (*)(void*, void*, void*, void*, void*, void*, void*, void*, void*, void*, void*, void*, void*, void*,
-                       void*, int, int, int, int, int, int, int, void*);
-    return reinterpret_cast<Fn>(g_fn[kAppend])(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], p[10], p[11], p[12],
-                                               p[13], p[14], B, Hkv, N, T, C, ldw, d, c.stream(15));
+    return FA_ENTRY(kAppend, fa_kv4_append)(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], p[10], p[11], p[12],
+                                            p[13], p[14], B, Hkv, N, T, C, ldw, d, c.stream(15));
   });
 }
 
@@ -192,16 +200,15 @@ PyObject* kv4_read(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor *kc = c.shaped(0, 4), *k = c.shaped(7, 4);
     if (c.bad) return -1;
     const int64_t B = kc->size(0), Hkv = kc->size(1), C = kc->size(2), half = kc->size(3), d = 2 * half, T = k->size(2);
-    void* p[9] = {c.get(0, U8, {B, Hkv, C, half}, true), c.get(1, BF16, {B, Hkv, C}, true),
-                  c.get(2, U8, {B, Hkv, C, half}, true), c.get(3, BF16, {B, Hkv, C}, true),
-                  c.get(4, F32, {d}, false),             c.get(5, I32, {B, Hkv, T}, false),
-                  c.get(6, I32, {B, Hkv}, false),        c.get(7, BF16, {B, Hkv, T, d}, true),
-                  c.get(8, BF16, {B, Hkv, T, d}, true)};
+    Ptr p[9] = {c.get(0, U8, {B, Hkv, C, half}, true), c.get(1, BF16, {B, Hkv, C}, true),
+                c.get(2, U8, {B, Hkv, C, half}, true), c.get(3, BF16, {B, Hkv, C}, true),
+                c.get(4, F32, {d}, false),             c.get(5, I32, {B, Hkv, T}, false),
+                c.get(6, I32, {B, Hkv}, false),        c.get(7, BF16, {B, Hkv, T, d}, true),
+                c.get(8, BF16, {B, Hkv, T, d}, true)};
     const int first = c.integer(9);
     if (c.bad || !fits_int({B, Hkv, T, C, d})) return -1;
-    using Fn = int (*)(void*, void*, void*, void*, void*, void*, void*, void*, void*, int, int, int, int, int, int, void*);
-    return reinterpret_cast<Fn>(g_fn[kRead])(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], B, Hkv, T, C, first, d,
-                                             c.stream(10));
+    return FA_ENTRY(kRead, fa_kv4_read)(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], B, Hkv, T, C, first, d,
+                                        c.stream(10));
   });
 }
 
@@ -211,18 +218,16 @@ PyObject* decode_kv4(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor *q = c.shaped(0, 3), *kc = c.shaped(1, 4), *ws = c.shaped(10, 1);
     if (c.bad) return -1;
     const int64_t B = kc->size(0), Hkv = kc->size(1), C = kc->size(2), half = kc->size(3), d = 2 * half, H = q->size(1);
-    void* p[11] = {c.get(0, BF16, {B, H, d}, true),        c.get(1, U8, {B, Hkv, C, half}, true),
-                   c.get(2, BF16, {B, Hkv, C}, true),      c.get(3, U8, {B, Hkv, C, half}, true),
-                   c.get(4, BF16, {B, Hkv, C}, true),      c.get(5, F32, {d}, false),
-                   c.get(6, I32, {B, Hkv}, true),          c.get(7, BF16, {B, H, d}, true),
-                   c.get(8, F32, {B, H}, true),            c.get(9, F32, {B, Hkv, C}, false),
-                   c.get(10, U8, {ws->size(0)}, true)};
+    Ptr p[11] = {c.get(0, BF16, {B, H, d}, true),        c.get(1, U8, {B, Hkv, C, half}, true),
+                 c.get(2, BF16, {B, Hkv, C}, true),      c.get(3, U8, {B, Hkv, C, half}, true),
+                 c.get(4, BF16, {B, Hkv, C}, true),      c.get(5, F32, {d}, false),
+                 c.get(6, I32, {B, Hkv}, true),          c.get(7, BF16, {B, H, d}, true),
+                 c.get(8, F32, {B, H}, true),            c.get(9, F32, {B, Hkv, C}, false),
+                 c.get(10, U8, {ws->size(0)}, true)};
     const float scale = static_cast<float>(c.number(11));
     if (c.bad || !fits_int({B, H, Hkv, C, d})) return -1;
-    using Fn = int (*)(void*, void*, void*, void*, void*, void*, void*, void*, void*, void*, int, int, int, int, int, float,
-                       void*, size_t, void*);
-    return reinterpret_cast<Fn>(g_fn[kDecode])(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], B, H, Hkv, C, d,
-                                               scale, p[10], ws->size(0), c.stream(12));
+    return FA_ENTRY(kDecode, fa_decode_kv4)(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], B, H, Hkv, C, d,
+                                            scale, p[10], ws->size(0), c.stream(12));
   });
 }
 

@@ -112,3 +112,22 @@ def test_a_module_that_could_not_be_built_again_is_gone(step):
     assert not os.path.exists(build.CALL)
     step.ok[0] = True
     assert step() and not step()
+
+
+def test_the_module_is_compiled_against_the_prototypes(tmp_path):
+    """A header that asks for one more argument: the module's six calls do not compile."""
+    import re
+
+    from exact_io_aware_85_b200 import build
+    (tmp_path / "pkg" / "csrc").mkdir(parents=True)
+    (tmp_path / "include").mkdir()
+    shutil.copy(os.path.join(build.CSRC, "call.cpp"), tmp_path / "pkg" / "csrc")
+    header = open(build.HEADER).read()
+    for f in ("fa_key_weights", "fa_evict_keep", "fa_evict_slots", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4"):
+        header, n = re.subn(rf"(int {f}\([^)]*)\)", r"\1, int more)", header)
+        assert n == 1, f
+    (tmp_path / "include" / "fa.h").write_text(header)
+    cmd = build.call_command(str(tmp_path / "out.so"))
+    cmd[cmd.index(os.path.join(build.CSRC, "call.cpp"))] = str(tmp_path / "pkg" / "csrc" / "call.cpp")
+    r = subprocess.run([*cmd, "-fsyntax-only"], capture_output=True, text=True, timeout=300)
+    assert r.returncode != 0 and r.stderr.count("too few arguments") == 6, r.stderr[-2000:]
