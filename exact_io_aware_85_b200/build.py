@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfa.so")
 LIB_DEBUG = os.path.join(PKG, "libfa_debug.so")
 SOURCES = ["api.cu", "sm100.cuh", "fwd.cuh", "bwd.cuh", "fp8.cuh", "decode.cuh", "fwd256.cuh", "bwd256.cuh",
-           "kv4.cuh", "evict.cuh", "key_weights.cuh", "api_cache.cuh"]
+           "early.cuh", "kv4.cuh", "evict.cuh", "key_weights.cuh", "api_cache.cuh"]
 CALL = os.path.join(PKG, "_fa_call.so")  # the cache operators' argument marshalling (csrc/call.cpp)
 CALL_STAMP = os.path.join(PKG, "_fa_call.stamp")  # what it was built with
 HEADER = os.path.join(os.path.dirname(PKG), "include", "fa.h")

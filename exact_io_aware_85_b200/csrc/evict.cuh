@@ -22,6 +22,7 @@
 // One row to take (a decoding step of a full cache) needs no search: one reduction over
 // (key, row) pairs.
 #pragma once
+#include "early.cuh"
 #include "sm100.cuh"
 
 namespace fa {

@@ -32,6 +32,7 @@
 //   warp 19      log-sum-exps of the steps' queries into operand tiles, read a step ahead
 // Tensor memory: two score tiles of 128 columns per key half.
 #pragma once
+#include "early.cuh"
 #include "sm100.cuh"
 
 namespace fa {

@@ -10,6 +10,7 @@
 // item 3): it spreads a key's outliers over the row before the row gets its one scale, and
 // (H a).(H b) = d a.b, so scores come from a rotated query and a factor 1/d.
 #pragma once
+#include "early.cuh"
 #include "sm100.cuh"
 
 namespace fa {
