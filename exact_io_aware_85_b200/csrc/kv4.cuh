@@ -401,8 +401,13 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
 //     (fp16 1024 + n and an addition instead: 594 instead of about 400 instructions per 32 keys
 //     of d = 128, and the same in bf16 for V.)
 //   * q in fp16, scaled by a power of two per head so that its largest element is near 2^14: a
-//     bf16 query is exact; a rotated query is held as a sum of two fp16 numbers (22 bits).  With
-//     at most four heads the second number sits in the MMA's unused columns.
+//     bf16 element within 2^27 of it is exact (odd ones, a sixteenth, are subnormals first); a
+//     rotated query is held as a sum of two fp16 numbers (22 bits).  With at most four heads the
+//     second number sits in the MMA's unused columns.
+//   * A score's accumulator starts at -8 sum(q) and meets up to 15 sum|q|: what it loses goes by
+//     sum|q|, whatever the codes are, d 2^-18 ks sum|q| at most (d / 16 steps, each of which may cut
+//     17 numbers at 2^-24 of the largest), measured 2^-17.7 with an element of q 2^14 times the
+//     others that meets zeros only.
 //   * P times the row's scale, u = p vs, meets V's codes in fp16 too (11 bits, so its rounding
 //     stays below that of the bf16 output).  Its range: p = 2^(x - R) with R a running maximum of
 //     x + log2 vs instead of x, so that u stays near one and what flushes is 2^-24 of the largest;

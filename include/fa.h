@@ -287,8 +287,13 @@ int fa_kv4_read(const void* kc, const void* ks, const void* vc, const void* vs, 
  * query head h reads key/value head h / (H / H_kv), at most 16 query heads share one.  signs:
  * as given to fa_kv4_append (the query is rotated inside).  A head with no rows gives o = 0 and
  * lse = -inf.  acc (or NULL): acc[b,hk,j] += the sum over the query heads that share hk of
- * their softmax weight of row j.  A query (rotated, where signs is given) of magnitudes below
- * 2^110 is taken exactly (22 bits where rotated).  Scales of V from 2^-80 to 2^90 cost no accuracy
+ * their softmax weight of row j.  A query's magnitudes (rotated, where signs is given) have to
+ * be below 2^110, and scale times them below 2^116.  It enters the products in steps of 2^-34
+ * of its head's largest element (of 2^-106, where that is smaller), so that a bf16 element within
+ * 2^27 of the largest is exact; rotated, with 22 bits.  The products are those of codes offset by
+ * 8, summed in fp32: a score is off by less than d 2^-18 scale s sum|q_i| (s the row's scale; q as
+ * rotated, / d), also where the large elements of q meet codes of zero (measured, at most
+ * 2^-17.7 scale s sum|q_i|).  Scales of V from 2^-80 to 2^90 cost no accuracy
  * (below, o keeps fewer bits; above, a row counts as weightless below 2^-126 max(vs) of the
  * weightiest).  workspace: >= fa_decode_kv4_workspace_bytes(..., weights = acc given); its
  * contents on entry do not matter, and calls that may run at the same time need one each.  Two

@@ -55,3 +55,49 @@ def test_queries_of_zeros_and_tiny_numbers_at_tiny_scales(d, g, rot):
                 if weights:
                     assert ((acc.cpu().double() - rw).abs() <= t_w.amax() * rw + 2.0 ** -22 * (1 + rw)).all(), where
                     assert (acc[:, :, lens:] == 0).all(), where
+
+
+# (rotated, the element's product with the keys' own rounding makes scores that a larger one would only drown)
+@pytest.mark.parametrize("d,g,rot,power", [(*v, p) for v in VARIANTS if v[1] in (1, 4, 8, 16) for p in ((8,) if v[2] else (8, 14))])
+def test_a_large_element_that_meets_zeros(d, g, rot, power):
+    """One element of the query 2^power times the others, where every key holds zero: it takes no part in a score, but
+    its products with the codes, held as c + 8, do, until 8 sum(q) leaves again.
+
+    Tolerance.  A score is scale ks (sum q_i n_i - 8 sum q_i), n_i = c_i + 8 <= 15, in the basis of the codes: an fp32
+    accumulator that starts at -8 sum q (d / 32 + 5 additions, each rounded to 2^-24 of 8 sum|q| at most) and takes
+    d / 16 products of 16 elements (twice that where q is held as two numbers), its contents at most 23 sum|q|.  Of the
+    17 numbers that such a step adds up, each may be cut at 2^-24 of the largest:
+    (d / 16 17 23 + (d / 32 + 5) 8) 2^-24 < d 2^-19 (d 2^-18 where held as two), times scale ks sum|q|."""
+    C, lens, signs = 512, 500, _signs(d, 7) if rot else None
+    q, k, v = _randn(1, 1, 2 * g, d), _randn(2, 1, 2, lens, d), _randn(3, 1, 2, lens, d)
+    q[..., 5] = 2.0 ** power
+    k[..., 5] = 0
+    scale = 1 / math.sqrt(d)
+    o, lse, acc, (ro, rl, rw, pv, terms), ks = _decode(q, k, v, lens, scale, signs, True, C)
+    qh = q.cpu().double() if signs is None else R.rotate(q.cpu().double(), signs.cpu()) / d
+    size = scale * ks.repeat_interleave(g, 1) * qh.abs().sum(-1)
+    es = d * 2.0 ** (-18 if rot else -19) * size
+    # terms of the scores in the codes' basis: at most 7 scale ks sum|q|
+    t_o, t_lse, t_w = _bounds(d, C, 7 * size if rot else terms, rl, pv, ro)
+    assert ((o.cpu().double() - ro).abs() <= t_o + 2 * es[..., None] * pv).all()
+    assert ((lse.cpu().double() - rl).abs() <= t_lse + es).all()
+    assert ((acc.cpu().double() - rw).abs() <= (t_w + 2 * es).amax() * rw + 2.0 ** -22 * (1 + rw)).all()
+
+
+@pytest.mark.parametrize("power", [-110, -100, -60, 60, 100])
+@pytest.mark.parametrize("rot", [False, True])
+def test_keys_of_any_size(rot, power):
+    """Keys far from one, with a softmax scale that brings the scores back."""
+    d, g, C, lens = 128, 4, 256, 200
+    signs = _signs(d, 4) if rot else None
+    k = (_randn(2, 1, 2, lens, d).float() * 2.0 ** power).to(torch.bfloat16)
+    q, v = _randn(1, 1, 2 * g, d), _randn(3, 1, 2, lens, d)
+    scale = 2.0 ** -power / math.sqrt(d)
+    o, lse, acc, (ro, rl, rw, pv, terms), ks = _decode(q, k, v, lens, scale, signs, True, C)
+    qh = q.cpu().double() if signs is None else R.rotate(q.cpu().double(), signs.cpu()) / d
+    size = scale * ks.repeat_interleave(g, 1) * qh.abs().sum(-1)       # see above
+    es = d * 2.0 ** (-18 if rot else -19) * size
+    t_o, t_lse, t_w = _bounds(d, C, 7 * size if rot else terms, rl, pv, ro)
+    assert ((o.cpu().double() - ro).abs() <= t_o + 2 * es[..., None] * pv).all()
+    assert ((lse.cpu().double() - rl).abs() <= t_lse + es).all()
+    assert ((acc.cpu().double() - rw).abs() <= (t_w + 2 * es).amax() * rw + 2.0 ** -22 * (1 + rw)).all()
