@@ -57,9 +57,10 @@ typedef enum {
   FA_ERR_UNSUPPORTED = 2, /* a head dim the entry point does not take (64 and 128
                              everywhere but fa_fwd_f32, which takes 64; 256 where
                              the entry point's comment says so), sizes over the
-                             limits above, B*H_kv > 65535 (fa_decode) or
-                             B*H > 65535 (fa_fp8_quantize), more than 16 query heads
-                             per key/value head (fa_decode), or a workspace larger
+                             limits above, B*H_kv > 65535 (fa_decode, fa_decode_kv4)
+                             or B*H > 65535 (fa_fp8_quantize), more than 16 query
+                             heads per key/value head (fa_decode, fa_decode_kv4), a
+                             scale below 2^-80 (fa_key_weights), or a workspace larger
                              than FA_BWD_NOALLOC_MAX_BYTES (fa_bwd_noalloc) */
   FA_ERR_ALIGNMENT = 3,   /* a pointer without the alignment the conventions require */
   FA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed */
