@@ -64,7 +64,7 @@ struct Kv4Rows {
   static constexpr int NE = D / 4, NP = NE / 2, BLOCKS = NE / 4;  // elements, pairs, groups of 4 of a lane and row
   static constexpr int WARPS = 4;                                 // per CTA
   static constexpr int CTAS = D == 256 ? 4 : 8;                   // per SM: 64 (128) registers a thread
-  static constexpr int RPL = 1, ROWS = 8 * RPL;                   // rows of a lane, of a warp
+  static constexpr int ROWS = 8;                                  // of a warp
 };
 
 // volatile, and told to touch memory: the load has to stay behind wait_for_earlier()
@@ -80,26 +80,23 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* r) {
                : "memory");
 }
 
-// B operand of the H16 MMAs: entry (k, n) is (-1)^popc(k & n), n the column of half `nt`; the
-// second of each pair of k times `odd`
+// Entry (k, n) of H16, the B operand of its MMAs: -1 to the number of ones of k & n.
 __device__ __forceinline__ float kv4_h16(int k, int n) { return (__popc(k & n) & 1) ? -1.f : 1.f; }
 
 // The stages of H between a lane's groups of 4 elements.
 template <int D>
-__device__ __forceinline__ void kv4_hadamard_groups(float2 (&z)[Kv4Rows<D>::RPL][Kv4Rows<D>::NP]) {
+__device__ __forceinline__ void kv4_hadamard_groups(float2 (&z)[Kv4Rows<D>::NP]) {
 #pragma unroll
   for (int h = 1; h < Kv4Rows<D>::BLOCKS; h <<= 1)
 #pragma unroll
     for (int b = 0; b < Kv4Rows<D>::BLOCKS; ++b)
       if (!(b & h))
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
-            const float2 p = z[r][2 * b + x], q = z[r][2 * (b + h) + x];
-            z[r][2 * b + x] = fadd2(p, q);
-            z[r][2 * (b + h) + x] = fsub2(p, q);
-          }
+        for (int x = 0; x < 2; ++x) {
+          const float2 p = z[2 * b + x], q = z[2 * (b + h) + x];
+          z[2 * b + x] = fadd2(p, q);
+          z[2 * (b + h) + x] = fsub2(p, q);
+        }
 }
 // three-input maximum of magnitudes in which a NaN wins
 __device__ __forceinline__ float absmax3_nan(float a, float b, float c) {
@@ -128,46 +125,33 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
   const int t0 = (blockIdx.x % a.tblocks) * (R::ROWS * R::WARPS) + warp * R::ROWS;
   const bool is_v = blockIdx.y == 1, rotate = !is_v && a.signs;
   const int n_new = a.n_new ? min(a.n_new[bh], a.T) : a.T;
-  int src[R::RPL];
-  long long dst[R::RPL];
-  bool live[R::RPL];
-  uint32_t w[R::RPL][R::NP];  // the rows' pairs of bf16
+  const int t = t0 + grp;
+  const long long bt = static_cast<long long>(bh) * a.T + t;
+  bool live = t < n_new;
+  const int src = live ? (a.rows ? a.rows[bt] : t) : -1;
+  const long long dst = live ? (a.slots ? a.slots[bt] : (a.start ? static_cast<long long>(a.start[bh]) : 0) + t) : -1;
+  live = src >= 0 && src < a.N && dst >= 0 && dst < a.C;
+  uint32_t w[R::NP];  // the row's pairs of bf16
+  const __nv_bfloat16* x = (is_v ? a.v : a.k) + (static_cast<size_t>(bh) * a.N + (live ? src : 0)) * D + tq * 16;
 #pragma unroll
-  for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
-    const int t = t0 + grp + 8 * r;
-    const long long bt = static_cast<long long>(bh) * a.T + t;
-    live[r] = t < n_new;
-    src[r] = live[r] ? (a.rows ? a.rows[bt] : t) : -1;
-    dst[r] = live[r] ? (a.slots ? a.slots[bt] : (a.start ? static_cast<long long>(a.start[bh]) : 0) + t) : -1;
-    live[r] = src[r] >= 0 && src[r] < a.N && dst[r] >= 0 && dst[r] < a.C;
-    const __nv_bfloat16* x = (is_v ? a.v : a.k) + (static_cast<size_t>(bh) * a.N + (live[r] ? src[r] : 0)) * D + tq * 16;
+  for (int u = 0; u < D / 64; ++u) {
+    if (live) ld_global_32(x + 64 * u, &w[8 * u]);
+    else
 #pragma unroll
-    for (int u = 0; u < D / 64; ++u) {
-      if (live[r]) ld_global_32(x + 64 * u, &w[r][8 * u]);
-      else
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[r][8 * u + i] = 0u;
-    }
+      for (int i = 0; i < 8; ++i) w[8 * u + i] = 0u;
   }
   const bool notes = !is_v && tq == 0;  // the lane that writes the row's weight and position
-  float weight[R::RPL];
-#pragma unroll
-  for (int r = 0; r < R::RPL; ++r)
-    weight[r] = notes && live[r] && a.acc && a.w ? a.w[static_cast<size_t>(bh) * a.ldw + src[r]] : 0.f;
+  const float weight = notes && live && a.acc && a.w ? a.w[static_cast<size_t>(bh) * a.ldw + src] : 0.f;
   const int base = notes && a.base ? a.base[bh / a.Hkv] : 0;
-  if (rotate) {  // (the rows are on their way)
+  if (rotate) {  // (the row is on its way)
     kv4_sign_masks<D>(a.signs, masks);
     __syncthreads();
   }
   if (t0 >= n_new) return;
-  float2 z[R::RPL][R::NP];
+  float2 z[R::NP];
   if (rotate) {
 #pragma unroll
-    for (int i = 0; i < R::NP; ++i) {
-      const uint32_t m = masks[32 * (i >> 3) + tq * 8 + (i & 7)];
-#pragma unroll
-      for (int r = 0; r < R::RPL; ++r) w[r][i] ^= m;
-    }
+    for (int i = 0; i < R::NP; ++i) w[i] ^= masks[32 * (i >> 3) + tq * 8 + (i & 7)];
     uint32_t b[2][2];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
@@ -179,71 +163,66 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
         float c[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_16816(c, w[0][2 * g], 0u, w[0][2 * g + 1], 0u, b[nt][0], b[nt][1]);
-        z[0][2 * g + nt] = make_float2(c[0], c[1]);
+        mma_16816(c, w[2 * g], 0u, w[2 * g + 1], 0u, b[nt][0], b[nt][1]);
+        z[2 * g + nt] = make_float2(c[0], c[1]);
       }
     kv4_hadamard_groups<D>(z);
   } else {
 #pragma unroll
-    for (int r = 0; r < Kv4Rows<D>::RPL; ++r)
-#pragma unroll
-      for (int i = 0; i < R::NP; ++i)
-        z[r][i] = make_float2(__uint_as_float(w[r][i] << 16), __uint_as_float(w[r][i] & 0xffff0000u));
+    for (int i = 0; i < R::NP; ++i)
+      z[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
+  float top = 0.f;
 #pragma unroll
-  for (int r = 0; r < Kv4Rows<D>::RPL; ++r) {
-    float top = 0.f;
+  for (int i = 0; i < R::NP; ++i) top = absmax3_nan(top, z[i].x, z[i].y);
+  top = absmax3_nan(top, __shfl_xor_sync(0xffffffffu, top, 1), 0.f);
+  top = absmax3_nan(top, __shfl_xor_sync(0xffffffffu, top, 2), 0.f);
+  const bool finite = top < INFINITY;
+  const __nv_bfloat16 sb = finite ? __float2bfloat16_rn(__fdiv_rn(top, 7.f))
+                                  : __ushort_as_bfloat16(static_cast<unsigned short>(0x7fff));
+  const float s = __bfloat162float(sb);
+  float2 c[R::NP];  // the codes less 8, whole numbers
+  if (finite && s >= 1e-30f) {
+    // |y| <= amax, so |c| <= 7 where s is a normal number.  With the rounded reciprocal one step on
+    // the remainder (an fma) gives the correctly rounded quotient (Markstein; s has 8 bits).
+    const float inv = __frcp_rn(s), kMagic = 12582912.f;  // 1.5 2^23
+    const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-s, -s), magic2 = make_float2(kMagic, kMagic);
 #pragma unroll
-    for (int i = 0; i < R::NP; ++i) top = absmax3_nan(top, z[r][i].x, z[r][i].y);
-    top = absmax3_nan(top, __shfl_xor_sync(0xffffffffu, top, 1), 0.f);
-    top = absmax3_nan(top, __shfl_xor_sync(0xffffffffu, top, 2), 0.f);
-    const bool finite = top < INFINITY;
-    const __nv_bfloat16 sb = finite ? __float2bfloat16_rn(__fdiv_rn(top, 7.f))
-                                    : __ushort_as_bfloat16(static_cast<unsigned short>(0x7fff));
-    const float s = __bfloat162float(sb);
-    float2 c[R::NP];  // the codes less 8, whole numbers
-    if (finite && s >= 1e-30f) {
-      // |y| <= amax, so |c| <= 7 where s is a normal number.  With the rounded reciprocal one step on
-      // the remainder (an fma) gives the correctly rounded quotient (Markstein; s has 8 bits).
-      const float inv = __frcp_rn(s), kMagic = 12582912.f;  // 1.5 2^23
-      const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-s, -s), magic2 = make_float2(kMagic, kMagic);
-#pragma unroll
-      for (int i = 0; i < R::NP; ++i) {
-        float2 q = fmul2(z[r][i], inv2);
-        q = ffma2(ffma2(q, neg2, z[r][i]), inv2, q);
-        c[i] = fsub2(fadd2(q, magic2), magic2);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < R::NP; ++i) {
-        const bool some = finite && s > 0.f;
-        c[i].x = some ? fminf(7.f, fmaxf(-7.f, rintf(__fdiv_rn(z[r][i].x, s)))) : 0.f;
-        c[i].y = some ? fminf(7.f, fmaxf(-7.f, rintf(__fdiv_rn(z[r][i].y, s)))) : 0.f;
-      }
+    for (int i = 0; i < R::NP; ++i) {
+      float2 q = fmul2(z[i], inv2);
+      q = ffma2(ffma2(q, neg2, z[i]), inv2, q);
+      c[i] = fsub2(fadd2(q, magic2), magic2);
     }
-    uint32_t packed[R::NE / 8];
+  } else {
 #pragma unroll
-    for (int i = 0; i < R::NE / 8; ++i) {
-      uint32_t half[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // c0 + 16 c1 + 256 c2 + 4096 c3, plus 0x8888, in the low bits of 2^23 + ...
-        const float2 t = ffma2(c[4 * i + 2 * h + 1], make_float2(256.f, 256.f), c[4 * i + 2 * h]);
-        half[h] = __float_as_uint(fmaf(t.y, 16.f, t.x) + (8388608.f + 34952.f));
-      }
-      packed[i] = __byte_perm(half[0], half[1], 0x5410);
+    for (int i = 0; i < R::NP; ++i) {
+      const bool some = finite && s > 0.f;
+      c[i].x = some ? fminf(7.f, fmaxf(-7.f, rintf(__fdiv_rn(z[i].x, s)))) : 0.f;
+      c[i].y = some ? fminf(7.f, fmaxf(-7.f, rintf(__fdiv_rn(z[i].y, s)))) : 0.f;
     }
-    if (!live[r]) continue;
-    const size_t row = static_cast<size_t>(bh) * a.C + dst[r];
-    uint8_t* codes = (is_v ? a.vc : a.kc) + row * (D / 2) + tq * 8;
+  }
+  uint32_t packed[R::NE / 8];
 #pragma unroll
-    for (int u = 0; u < D / 64; ++u) *reinterpret_cast<uint2*>(codes + 32 * u) = make_uint2(packed[2 * u], packed[2 * u + 1]);
-    if (tq == 0) {
-      (is_v ? a.vs : a.ks)[row] = sb;
-      if (!is_v) {
-        if (a.acc) a.acc[row] = weight[r];
-        if (a.pos) a.pos[row] = base + src[r];
-      }
+  for (int i = 0; i < R::NE / 8; ++i) {
+    uint32_t half[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // c0 + 16 c1 + 256 c2 + 4096 c3, plus 0x8888, in the low bits of 2^23 + ...
+      const float2 p = ffma2(c[4 * i + 2 * h + 1], make_float2(256.f, 256.f), c[4 * i + 2 * h]);
+      half[h] = __float_as_uint(fmaf(p.y, 16.f, p.x) + (8388608.f + 34952.f));
+    }
+    packed[i] = __byte_perm(half[0], half[1], 0x5410);
+  }
+  if (!live) return;
+  const size_t row = static_cast<size_t>(bh) * a.C + dst;
+  uint8_t* codes = (is_v ? a.vc : a.kc) + row * (D / 2) + tq * 8;
+#pragma unroll
+  for (int u = 0; u < D / 64; ++u) *reinterpret_cast<uint2*>(codes + 32 * u) = make_uint2(packed[2 * u], packed[2 * u + 1]);
+  if (tq == 0) {
+    (is_v ? a.vs : a.ks)[row] = sb;
+    if (!is_v) {
+      if (a.acc) a.acc[row] = weight;
+      if (a.pos) a.pos[row] = base + src;
     }
   }
 }
@@ -335,7 +314,7 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
   if (!a.signs) {
     plain(w[0], s[0]);
   } else {
-    float2 z[R::RPL][R::NP];
+    float2 z[R::NP];
     uint32_t b[2][2];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
@@ -355,20 +334,20 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
       for (int nt = 0; nt < 2; ++nt) {
         float c[4] = {0.f, 0.f, 0.f, 0.f};
         mma_16816_f16(c, p[0], 0u, p[1], 0u, b[nt][0], b[nt][1]);
-        z[0][2 * g + nt] = make_float2(c[0], c[1]);
+        z[2 * g + nt] = make_float2(c[0], c[1]);
       }
     }
     kv4_hadamard_groups<D>(z);
-    if (tq == 0) z[0][0].x -= 8.f * D / 1024.f;
+    if (tq == 0) z[0].x -= 8.f * D / 1024.f;
     float f = s[0] * (1024.f / D);
     if (s[0] > 1e30f) {  // the product of the factors could pass fp32's range
       f = s[0];
 #pragma unroll
-      for (int i = 0; i < R::NP; ++i) z[0][i] = fmul2(z[0][i], make_float2(1024.f / D, 1024.f / D));
+      for (int i = 0; i < R::NP; ++i) z[i] = fmul2(z[i], make_float2(1024.f / D, 1024.f / D));
     }
 #pragma unroll
     for (int i = 0; i < R::NP; ++i) {
-      const float2 v = fmul2(z[0][i], make_float2(f, f));
+      const float2 v = fmul2(z[i], make_float2(f, f));
       x[i] = pack_bf16x2(v.x, v.y) ^ masks[32 * (i >> 3) + tq * 8 + (i & 7)];
     }
   }
