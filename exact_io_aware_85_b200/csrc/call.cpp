@@ -21,7 +21,21 @@ namespace {
 void* g_fn[6];  // addresses of the library's entry points, in the order of `bind`
 enum { kKeyWeights, kEvictKeep, kEvictSlots, kAppend, kRead, kDecode };
 // one of them, called by its prototype in fa.h
-#define FA_ENTRY(i, f) reinterpret_cast<decltype(&f)>(g_fn[i])
+#define FA_ENTRY(i, f) Entry<decltype(&f)>{reinterpret_cast<decltype(&f)>(g_fn[i])}
+// ... with the interpreter's lock let go: a launch blocks while the stream's queue is full, and what is queued
+// before it may need a Python thread
+template <typename F>
+struct Entry {
+  F f;
+  template <typename... A>
+  int operator()(A... a) const {
+    int status;
+    Py_BEGIN_ALLOW_THREADS;
+    status = f(a...);
+    Py_END_ALLOW_THREADS;
+    return status;
+  }
+};
 
 constexpr auto BF16 = at::ScalarType::BFloat16;
 constexpr auto F32 = at::ScalarType::Float;
