@@ -90,3 +90,47 @@ def test_rows_read_and_appended_right_behind(how, d, rot):
     for x, y in zip([*want[0], *want[1], *want[2:]], [*got[0], *got[1], *got[2:]]):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
     assert bool(want[3].float().abs().sum() > 0)
+
+
+@pytest.mark.gpu
+def test_calls_at_the_same_time():
+    """Decoding steps and key weights on two streams, a workspace each, over the same cache and prompt: the bits of
+    the calls alone."""
+    from exact_io_aware_85_b200 import fa
+    B, H, Hkv, N, C, d = 2, 8, 2, 900, 4096, 128
+    g = torch.Generator().manual_seed(8)
+    rnd = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    q, k, v, ck, cv = rnd(B, H, N, d), rnd(B, Hkv, N, d), rnd(B, Hkv, N, d), rnd(B, Hkv, C, d), rnd(B, Hkv, C, d)
+    o, lse = torch.empty_like(q), torch.empty((B, H, N), device=DEV)
+    fa.fa_fwd_gqa(q, k, v, o, lse, True, d ** -0.5)
+    cache = [torch.zeros((B, Hkv, C, d // 2), dtype=torch.uint8, device=DEV), torch.zeros((B, Hkv, C), dtype=torch.bfloat16, device=DEV)]
+    cache += [t.clone() for t in cache]
+    fa.fa_kv4_append(ck, cv, *cache)
+    lens = torch.tensor([[C, 5], [77, 3000]], dtype=torch.int32, device=DEV)
+    qs = [rnd(B, H, d) for _ in range(2)]
+
+    def buffers():
+        return dict(o=torch.zeros_like(qs[0]), lse=torch.zeros((B, H), device=DEV), acc=torch.zeros((B, Hkv, C), device=DEV),
+                    w=torch.zeros((B, Hkv, N), device=DEV),
+                    ws=torch.empty(fa.fa_decode_kv4_workspace_bytes(B, H, Hkv, C, d, True), dtype=torch.uint8, device=DEV),
+                    wk=torch.empty(fa.fa_key_weights_workspace_bytes(B, H, Hkv, N, d, 300), dtype=torch.uint8, device=DEV))
+
+    def calls(b, i, stream):
+        for _ in range(6):
+            fa.fa_decode_kv4(qs[i], *cache, lens, b["o"], b["lse"], 0.1, b["ws"], acc=b["acc"], stream=stream)
+            fa.fa_key_weights(q, k, lse, b["w"], True, d ** -0.5, b["wk"], window=300, stream=stream)
+
+    want = [buffers(), buffers()]
+    for i in (0, 1):
+        calls(want[i], i, None)
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [buffers(), buffers()]
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            calls(got[i], i, streams[i])
+        torch.cuda.synchronize()
+        assert fa.fa_check_status() == fa.FA_OK
+        for x, y in zip(want, got):
+            assert all(torch.equal(x[n], y[n]) for n in ("o", "lse", "acc", "w"))
