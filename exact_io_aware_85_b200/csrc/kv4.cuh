@@ -397,9 +397,10 @@ __global__ void __launch_bounds__(32 * Kv4Rows<D>::WARPS, Kv4Rows<D>::CTAS) fa_k
 //
 // Measured, both kernels, codes from DRAM: 64 heads of 32768 rows of d = 128, four query heads
 // each, weights wanted: 68 us (69 when every lane went on with all 32 keys instead of SPLIT below;
-// the bytes 45 at the copy rate; the issue slots are 56 % busy, and the scores' store and the
-// weights' kernel cost some 13 us); 64 ragged heads of up to 16384 rows of d = 256, eight query
-// heads each: 48 us (21); 8 heads of 1000 rows of d = 64: 8 us, two launches' latency.
+// the bytes 45 at the copy rate; the issue slots are 54 % busy), without weights 53 us (42): the
+// scores' store and the second kernel's part in them are 16 us; eight query heads each 84 and 60 us,
+// sixteen 178 and 100 us; 64 ragged heads of up to 16384 rows of d = 256, eight query heads each:
+// 48 us (21), sixteen 78 us; 8 heads of 1000 rows of d = 64: 8 us, two launches' latency.
 struct Kv4DecodeArgs {
   const __nv_bfloat16* q;  // [B*H, d]
   const float* signs;      // [d] or null
